@@ -401,3 +401,12 @@ def dsa_cp_merge(outs, lses, out, lse, ws, stream=None) -> None:
     ranks, n_q, H, dv = (int(x) for x in outs.shape)
     _check(lib().dsa_cp_merge(_ptr(outs), _ptr(lses), ranks, n_q, H, dv, _ptr(out), _ptr(lse),
                               _ptr(ws), ws.numel(), _stream(stream)), "dsa_cp_merge")
+
+
+# the 4-bit latent cache, attention mass and eviction (include/dsa_l4.h)
+from .latent4 import (  # noqa: E402,F401
+    EVICT_MAX_POOLS, Eviction, L4_EXPORTED, L4_OP_ATTENTION_FORWARD, L4_OP_ATTENTION_MASS,
+    L4_OP_CACHE_EVICT, L4_OP_SPARSE_MLA, L4_OP_STATUS, dsa_attention_forward_l4,
+    dsa_attention_mass, dsa_attention_mass_l4, dsa_attention_mass_l8, dsa_cache_append_l4,
+    dsa_cache_evict, dsa_cache_read_l4, dsa_sparse_mla_decode_l4, dsa_sparse_mla_prefill_l4,
+    l4_row_bytes, l4_workspace, l4_workspace_bytes)

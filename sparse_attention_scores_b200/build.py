@@ -36,7 +36,7 @@ def needs_build() -> bool:
         return True
     t = os.path.getmtime(LIB_PATH)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    deps.append(os.path.join(PKG_DIR, "..", "include", "dsa.h"))
+    deps += glob.glob(os.path.join(PKG_DIR, "..", "include", "*.h"))
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
