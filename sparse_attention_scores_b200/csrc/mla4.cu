@@ -4,11 +4,34 @@
 //   z[h, j]   = scale * q[h, :] . L[idx_j, :],   L = 2^e * s * v
 //   out[h, :] = sum_j softmax_j(z[h, :]) * L[idx_j, 0:R],   lse[h] = log sum_j exp z[h, j]
 //
-// One CTA of eight warps per (query row, eight heads), one warp per head:
-// chunks of kKeys selected rows are decoded into shared memory as fp16 (s * v,
-// exact), the warp forms its logits by dot products over its lanes, and keeps
-// a running maximum and sum; lane l accumulates the output columns l, l + 32,
-// ... in fp32 registers.  Everything is fp32 on CUDA cores.
+// Every s * v has at most 6 significant bits and lies in [2^-10, 2688]: an
+// fp16 value.  So the selected rows are widened to fp16 tiles in shared memory
+// (exactly) and both products run on tcgen05 in kind::f16 with fp16 operands:
+//   S = Q . L^T   M = 64 heads, N = 64 keys, K = R + P      (Q: fp16, below)
+//   O^T += L^T . P^T   M = 128 latent columns per block, N = 64 heads, K = 64 keys
+// The row's 2^e stays out of the tiles.  In base-2 units, with z2 = z log2(e):
+//   w[h, j] = 2^(z2 + e_j - m_h),  m_h a running maximum of z2 + e_j,
+//   out = sum w s v / sum w 2^-e_j,   lse = (m + log2 sum w 2^-e_j) ln 2
+// so weights stay in (0, 1] whatever the tokens' sizes (|e| <= 60 keeps every
+// factor inside fp32), and enter the second product as two fp16 terms, hi + lo
+// (22 bits), scaled by 2^6.  q enters as fp16 after one power of two per query
+// row that puts its largest magnitude in [2^14, 2^15).
+//
+// One CTA per SM takes a contiguous run of 64-key slots of one query row:
+//   warps 0-3    query tile; softmax of each slot (warp w: heads 16 w ..),
+//                the rare rescale of O
+//   warps 4-11   widening: warp 4 + g decodes rows 8 g .. 8 g + 7 of a slot
+//                from registers, where the next slot's bytes are already
+//                being loaded
+//   warp 12      one thread issues the MMAs: S of a slot as soon as it is
+//                widened, its PV product as soon as its weights are written
+// Two slots of the tile ring; S is double-buffered in tensor memory, so S of
+// one slot runs under the softmax of the other, and widening under both
+// products.  P hi goes over the slot's own atom that only S reads (the rope
+// atom at R = 512), P lo into one buffer that the PV product reads first.
+//
+// A row split over several CTAs leaves (m, l, O) partials in global scratch
+// (they stay in L2) and a merge kernel combines them.
 #include <math.h>
 
 #include <algorithm>
@@ -18,10 +41,19 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHeadsPerCta = kThreads / 32;
-constexpr int kKeys = 32;
-constexpr int kMaxPairs = 9;  // column pairs per lane: 576 / 64
+constexpr int kThreads = 416;
+constexpr int kSoftWarps = 4;
+constexpr int kWideWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kWideWarps;
+constexpr int kHeads = 64;
+constexpr int kKeys = 64;              // keys per slot
+constexpr int kAtom = kKeys * 128;     // bytes of a 64-column atom of 64 rows (tile or query)
+constexpr int kMaxUnits = 5;           // 16-byte code units per lane: 18 at W = 576, over 4 lanes
+constexpr int kWeightLog2 = 6;         // weights enter the tensor cores scaled by 2^6
+constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceeded by 2^8
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kMisc = 1536;
+constexpr int kMaxSplits = 148;
 
 struct Mla4Params {
   const uint16_t *q;
@@ -30,105 +62,659 @@ struct Mla4Params {
   const int32_t *idx;
   float *out;
   float *lse;
-  int H, R, W, topk;
-  float scale;
+  float *part_o;   // [n_q, nsplit, H, R]      (nsplit > 1)
+  float *part_ml;  // [n_q, nsplit, 2, H]
+  int n_q, H, R, W, topk, nsplit;
+  float scale_log2;
+  uint64_t wait_ns;
+  int debug_stall;
   DevStatus *status;
 };
 
-__global__ void __launch_bounds__(kThreads) mla4_simple_kernel(const Mla4Params p) {
-  __shared__ __half2 tile[kKeys][288];
-  __shared__ float two_e[kKeys];
-  __shared__ int rowi[kKeys];
+struct Layout {
+  int nQ, nmb, nL;    // query atoms, 128-column blocks of O^T, atoms per slot
+  int hi_atom;        // the slot's atom that P hi overlays, -1: buffers of its own
+  uint32_t off_q, off_hi, off_lo, off_misc, bytes;
+};
+__host__ __device__ inline Layout layout_of(int R, int W) {
+  Layout l;
+  l.nQ = (W + 63) / 64;
+  l.nmb = (R + 127) / 128;
+  l.nL = l.nQ > 2 * l.nmb ? l.nQ : 2 * l.nmb;
+  l.hi_atom = l.nL > 2 * l.nmb ? 2 * l.nmb : -1;
+  l.off_q = 2u * l.nL * kAtom;
+  l.off_hi = l.off_q + static_cast<uint32_t>(l.nQ) * kAtom;
+  l.off_lo = l.off_hi + (l.hi_atom < 0 ? 2u * kAtom : 0u);
+  l.off_misc = l.off_lo + kAtom;
+  l.bytes = l.off_misc + kMisc;
+  return l;
+}
+
+// barrier over `n` threads that also returns whether any of them passed true
+__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// bounded wait that also gives up as soon as another role has failed
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                             volatile uint32_t *failed) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*failed) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *failed = 1u;
+      return false;
+    }
+  }
+}
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// 16 lanes x 64 columns: thread t gets columns 8 i + 2 (t % 4) + {0, 1} of lane
+// t / 4 in r[4 i], r[4 i + 1] and of lane t / 4 + 8 in r[4 i + 2], r[4 i + 3]
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int W = p.W, R = p.R;
+  const Layout lay = layout_of(R, W);
+  const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q, lo_buf = tile + lay.off_lo;
+  const uint32_t slot_bytes = static_cast<uint32_t>(lay.nL) * kAtom;
+  const uint32_t hi_base = lay.hi_atom >= 0 ? tile + lay.hi_atom * kAtom : tile + lay.off_hi;
+  const uint32_t hi_step = lay.hi_atom >= 0 ? slot_bytes : kAtom;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
+  uint64_t *full = bars;        // [2] slot widened (one arrive per widening warp)
+  uint64_t *empty = bars + 2;   // [2] PV of the slot completed (MMA commit)
+  uint64_t *sfull = bars + 4;   // [2] S of the slot in tensor memory (MMA commit)
+  uint64_t *pready = bars + 6;  // the current slot's weights written (one arrive per softmax warp)
+  uint64_t *lofree = bars + 7;  // P lo of the current slot read (MMA commit)
+  uint64_t *qready = bars + 8;  // query tile written (one arrive per softmax warp)
+  uint64_t *bar_drain = bars + 9;
+  uint64_t *bar_stall = bars + 10;
+  // [0] tensor memory base, [1] failed
+  volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 12);
+  volatile uint32_t *failed = misc + 1;
+  float *qmax = reinterpret_cast<float *>(bars + 14);   // [4]
+  float *alpha = qmax + 4;                              // [64]
+  float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);  // [2][64] (2^e, e); (0, -inf): unused
+  float *mfin = reinterpret_cast<float *>(smem + lay.off_lo);  // [64], [64]: after the loop
+  float *lfin = mfin + kHeads;
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int split = blockIdx.x;
+  // causal rows grow with their number: the longest ones start first
+  const int row = p.rows.causal ? p.n_q - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
+
+  // tensor memory: S of slot s at columns 64 s, O^T from column 128
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < static_cast<uint32_t>(2 * kKeys + lay.nmb * kHeads)) tmem_cols <<= 1;
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&full[s], kWideWarps);
+      mbar_init(&empty[s], 1);
+      mbar_init(&sfull[s], 1);
+    }
+    mbar_init(pready, kSoftWarps);
+    mbar_init(lofree, 1);
+    mbar_init(qready, kSoftWarps);
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_stall, 1);
+    *failed = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(const_cast<uint32_t *>(&misc[0]), tmem_cols);
+    tmem_relinquish();
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.x, warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
-  const int h = blockIdx.y * kHeadsPerCta + warp;
-  const int W = p.W, pairs = W / 2, nb = W / kL4Block;
-  const int len = l4_row_len(p.rows, r), limit = l4_limit(p.rows, len);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  if (p.debug_stall) {
+    if (tid == 0 && !mbar_wait(bar_stall, 0u, p.wait_ns)) *failed = 1u;
+    __syncthreads();
+  }
+
+  // this CTA's slots: a row keeps at most min(topk, len) tokens, in its first
+  // places, and its slots are shared out evenly over the splits
+  const int len = l4_row_len(p.rows, row);
+  const int limit = l4_limit(p.rows, len);
   const int nsel = max(0, min(p.topk, len));
-  float2 q[kMaxPairs], acc[kMaxPairs];
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int c = lane + 32 * i;
-    q[i] = acc[i] = make_float2(0.f, 0.f);
-    if (c < pairs && h < p.H) {
-      const uint32_t v = reinterpret_cast<const uint32_t *>(
-          p.q + (static_cast<int64_t>(r) * p.H + h) * W)[c];
-      q[i] = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  const int nh_row = (nsel + kKeys - 1) / kKeys;
+  const int per = (nh_row + p.nsplit - 1) / p.nsplit;
+  const int h_begin = min(nh_row, split * per);
+  const int nh = min(nh_row, h_begin + per) - h_begin;
+
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------- query tile, softmax
+    // the 64-head query tile (heads >= H zero), 128B-swizzled, K-major; first
+    // as bf16, then scaled to fp16 in place by the threads that loaded it
+    const int cpr = W / 8;  // 16-byte pieces per row
+    if (nh > 0) {
+      const uint16_t *qrow = p.q + static_cast<int64_t>(row) * p.H * W;
+      for (int h = warp; h < kHeads; h += kSoftWarps)
+        for (int c = lane; c < cpr; c += 32) {
+          const bool ok = h < p.H;
+          cp_async_16(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4),
+                      ok ? qrow + h * W + c * 8 : p.q, ok ? 16u : 0u);
+        }
+      cp_async_commit();
+      cp_async_wait_all();
     }
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j0 = 0; j0 < nsel; j0 += kKeys) {
-    __syncthreads();
-    if (tid < kKeys) {
-      const int j = j0 + tid;
-      const int pos = j < nsel ? p.idx[static_cast<int64_t>(r) * p.topk + j] : -1;
-      const int row = l4_pool_row(p.rows, r, pos, limit, blockIdx.y == 0 ? p.status : nullptr,
-                                  kKernMla4, j);
-      rowi[tid] = row;
-      two_e[tid] = row < 0 ? 0.f
-                           : pow2i(l4_exponent(p.latent[static_cast<int64_t>(row) * l4_row_bytes(W) +
-                                                        W / 2 + nb]));
+    float zscale;  // logit units: log2(e) * scale / the query's power of two
+    {
+      float mx = 0.f;
+      if (nh > 0)
+        for (int h = warp; h < kHeads; h += kSoftWarps)
+          for (int c = lane; c < cpr; c += 32) {
+            const uint4 v = lds_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
+                                   fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
+          }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) qmax[warp] = mx;
+      bar_sync(1, 32 * kSoftWarps);
+      mx = fmaxf(fmaxf(qmax[0], qmax[1]), fmaxf(qmax[2], qmax[3]));
+      const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+      const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
+      const float f = pow2i(k);
+      zscale = p.scale_log2 * pow2i(-k);
+      if (nh > 0)
+        for (int h = warp; h < kHeads; h += kSoftWarps)
+          for (int c = lane; c < cpr; c += 32) {
+            const uint32_t a = qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4);
+            const uint4 v = lds_v4(a);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              o[t] = pack_f16(__uint_as_float(w[t] << 16) * f,
+                              __uint_as_float(w[t] & 0xFFFF0000u) * f);
+            sts_v4(a, o[0], o[1], o[2], o[3]);
+          }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
     }
-    __syncthreads();
-    for (int u = tid; u < kKeys * nb; u += kThreads) {
-      const int k = u / nb, b = u % nb;
-      uint32_t hv[4];
-      if (rowi[k] < 0) continue;
-      const uint8_t *src = p.latent + static_cast<int64_t>(rowi[k]) * l4_row_bytes(W);
-      const uint2 c = *reinterpret_cast<const uint2 *>(src + 8 * b);
-      const __half2 s = e4m3_to_half2(src[W / 2 + b]);
+    const int r0 = lane >> 2, c2 = 2 * (lane & 3);
+    const int h0 = 16 * warp + r0, h1 = h0 + 8;  // this thread's two heads
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t prow0 = h0 * 128, prow1 = h1 * 128, pcol = c2 * 2;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool alive = true;
+    for (int j = 0; j < nh; ++j) {
+      const int s = j & 1;
+      const uint32_t par = (j >> 1) & 1;
+      alive = alive && wait_or_fail(&sfull[s], par, p.wait_ns, failed) &&
+              wait_or_fail(&full[s], par, p.wait_ns, failed);
+      tc_fence_after();
+      // z2 + e of this thread's 16 keys of two heads
+      uint32_t v[32];
+      tmem_ld_16x256b_x8(tmem + lane_off + kKeys * s, v);
+      tmem_ld_wait();
+      float inv[16];  // 2^-e of the 16 keys
+      float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        e2m1x8_to_f16x2(half ? c.y : c.x, hv);
+      for (int i = 0; i < 8; ++i) {
+        const float4 k = *reinterpret_cast<const float4 *>(&keys[s * kKeys + 8 * i + c2]);
+        const float ka = k.x * zscale, kb = k.z * zscale;
+        inv[2 * i] = __uint_as_float((254u << 23) - __float_as_uint(k.x));
+        inv[2 * i + 1] = __uint_as_float((254u << 23) - __float_as_uint(k.z));
+        const float a0 = fmaf(__uint_as_float(v[4 * i]), ka, k.y);
+        const float b0 = fmaf(__uint_as_float(v[4 * i + 1]), kb, k.w);
+        const float a1 = fmaf(__uint_as_float(v[4 * i + 2]), ka, k.y);
+        const float b1 = fmaf(__uint_as_float(v[4 * i + 3]), kb, k.w);
+        x0 = fmaxf(x0, fmaxf(a0, b0));
+        x1 = fmaxf(x1, fmaxf(a1, b1));
+        v[4 * i] = __float_as_uint(a0);
+        v[4 * i + 1] = __float_as_uint(b0);
+        v[4 * i + 2] = __float_as_uint(a1);
+        v[4 * i + 3] = __float_as_uint(b1);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tile[k][8 * b + 4 * half + i] = __hmul2(as_half2(hv[i]), s);
+      for (int o = 1; o < 4; o <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+      }
+      float a0 = 1.f, a1 = 1.f;
+      if (x0 > m0 + kRescaleLog2 || m0 == -INFINITY) {
+        a0 = x0 == m0 ? 1.f : ex2(m0 - x0);
+        m0 = x0;
+      }
+      if (x1 > m1 + kRescaleLog2 || m1 == -INFINITY) {
+        a1 = x1 == m1 ? 1.f : ex2(m1 - x1);
+        m1 = x1;
+      }
+      const bool need = j > 0 && ((a0 != 1.f && h0 < p.H) || (a1 != 1.f && h1 < p.H));
+      if (bar_or(1, 32 * kSoftWarps, need || !alive)) {
+        // O holds every earlier slot once PV(j - 1) has completed
+        if (bar_or(1, 32 * kSoftWarps, !alive)) break;
+        if ((lane & 3) == 0) {
+          alpha[h0] = a0;
+          alpha[h1] = a1;
+        }
+        alive = wait_or_fail(&empty[(j - 1) & 1], ((j - 1) >> 1) & 1, p.wait_ns, failed);
+        bar_sync(1, 32 * kSoftWarps);
+        tc_fence_after();
+        if (alive)
+          for (int u = 0; u < 2 * lay.nmb; ++u) {
+            const uint32_t ta = tmem + lane_off + 2 * kKeys + 32 * u;
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(ta, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[32 * (u & 1) + i]);
+            tmem_st_32x32b_x32(ta, o);
+          }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        bar_sync(1, 32 * kSoftWarps);  // alpha may be rewritten
+      }
+      // weights, 2^6 of them, and their share of l
+      const float f0 = (m0 == -INFINITY ? 0.f : m0) - kWeightLog2;
+      const float f1 = (m1 == -INFINITY ? 0.f : m1) - kWeightLog2;
+      float s0 = 0.f, s1 = 0.f;
+      uint32_t lw0[8], lw1[8];
+      const uint32_t hb = hi_base + s * hi_step;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wa0 = ex2(__uint_as_float(v[4 * i]) - f0), wb0 = ex2(__uint_as_float(v[4 * i + 1]) - f0);
+        const float wa1 = ex2(__uint_as_float(v[4 * i + 2]) - f1), wb1 = ex2(__uint_as_float(v[4 * i + 3]) - f1);
+        s0 = fmaf(wb0, inv[2 * i + 1], fmaf(wa0, inv[2 * i], s0));
+        s1 = fmaf(wb1, inv[2 * i + 1], fmaf(wa1, inv[2 * i], s1));
+        const uint32_t hi0 = pack_f16(wa0, wb0), hi1 = pack_f16(wa1, wb1);
+        const float2 g0 = __half22float2(as_half2(hi0)), g1 = __half22float2(as_half2(hi1));
+        lw0[i] = pack_f16(wa0 - g0.x, wb0 - g0.y);
+        lw1[i] = pack_f16(wa1 - g1.x, wb1 - g1.y);
+        const uint32_t ch = static_cast<uint32_t>((i ^ r0) << 4) + pcol;  // h0 % 8 = h1 % 8 = r0
+        sts_u32(hb + prow0 + ch, hi0);
+        sts_u32(hb + prow1 + ch, hi1);
+      }
+      l0 = fmaf(l0, a0, s0);
+      l1 = fmaf(l1, a1, s1);
+      if (j > 0) alive = wait_or_fail(lofree, (j - 1) & 1, p.wait_ns, failed) && alive;
+      if (alive) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t ch = static_cast<uint32_t>((i ^ r0) << 4) + pcol;
+          sts_u32(lo_buf + prow0 + ch, lw0[i]);
+          sts_u32(lo_buf + prow1 + ch, lw1[i]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && alive) mbar_arrive(pready);
+    }
+    // the last PV has to complete before O and the lo buffer are used
+    if (nh > 0) wait_or_fail(&empty[(nh - 1) & 1], ((nh - 1) >> 1) & 1, p.wait_ns, failed);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    bar_sync(1, 32 * kSoftWarps);
+    if ((lane & 3) == 0) {
+      const bool good = nh > 0 && !*failed;
+      mfin[h0] = good ? m0 - kWeightLog2 : -INFINITY;
+      mfin[h1] = good ? m1 - kWeightLog2 : -INFINITY;
+      lfin[h0] = good ? l0 : 0.f;
+      lfin[h1] = good ? l1 : 0.f;
+    }
+  } else if (warp < kMmaWarp) {
+    // -------------------------------------------------------------- widening
+    // lane: row r8 of the warp's eight, every fourth 16-byte code unit from sub
+    const int g = warp - kSoftWarps, r8 = lane & 7, sub = lane >> 3;
+    const int nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
+    const int32_t *idx = p.idx + static_cast<int64_t>(row) * p.topk;
+    auto resolve = [&](int j) -> int {
+      const int place = (h_begin + j) * kKeys + 8 * g + r8;
+      if (j >= nh || place >= nsel) return -1;
+      return l4_pool_row(p.rows, row, idx[place], limit, sub == 0 ? p.status : nullptr, kKernMla4,
+                         place);
+    };
+    uint4 code[kMaxUnits];
+    uint32_t sc[kMaxUnits], eb = 127u;
+    auto load = [&](int phys) {
+      const uint8_t *src = p.latent + static_cast<int64_t>(phys < 0 ? 0 : phys) * rb;
+#pragma unroll
+      for (int i = 0; i < kMaxUnits; ++i) {
+        const int u = sub + 4 * i;
+        code[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = 0u;
+        if (phys >= 0 && u < units) {
+          code[i] = *reinterpret_cast<const uint4 *>(src + 16 * u);
+          sc[i] = *reinterpret_cast<const uint16_t *>(src + W / 2 + 2 * u);
+        }
+      }
+      if (sub == 0 && phys >= 0) eb = src[W / 2 + nb];
+    };
+    int phys = resolve(0);
+    load(phys);
+    int phys_next = resolve(1);
+    for (int j = 0; j < nh; ++j) {
+      const int s = j & 1;
+      if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+      const uint32_t base = tile + s * slot_bytes + (8 * g + r8) * 128;
+#pragma unroll
+      for (int i = 0; i < kMaxUnits; ++i) {
+        const int u = sub + 4 * i;
+        if (u < units) {
+          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+          const __half2 s_lo = e4m3_to_half2(sc[i]), s_hi = e4m3_to_half2(sc[i] >> 8);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (t >= 2 && 2 * u + 1 >= nb) break;  // W = 16 (mod 32): the unit's second block is no column
+            uint32_t h[4];
+            e2m1x8_to_f16x2(w[t], h);
+            const __half2 sv = t < 2 ? s_lo : s_hi;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __half2 x = __hmul2(as_half2(h[q]), sv);
+              h[q] = *reinterpret_cast<const uint32_t *>(&x);
+            }
+            const uint32_t ch = static_cast<uint32_t>((4 * (u & 1) + t) ^ r8) << 4;
+            sts_v4(base + (u >> 1) * kAtom + ch, h[0], h[1], h[2], h[3]);
+          }
+        }
+      }
+      if (sub == 0) {
+        const int e = l4_exponent(eb);
+        keys[s * kKeys + 8 * g + r8] =
+            phys >= 0 ? make_float2(pow2i(e), static_cast<float>(e)) : make_float2(0.f, -INFINITY);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      phys = phys_next;
+      load(phys);
+      phys_next = resolve(j + 2);
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------- MMA issue
+    const uint32_t idesc_s = idesc_f16_f32(kHeads, kKeys, 0);
+    const uint32_t idesc_pv = idesc_f16_f32(128, kHeads, 1);
+    const uint64_t d_q = smem_desc(qs, 16, 1024, kLayoutSW128);
+    const uint64_t d_lo = smem_desc(lo_buf, 16, 1024, kLayoutSW128);
+    uint64_t d_l[2], d_v[2], d_hi[2];
+    for (int s = 0; s < 2; ++s) {
+      d_l[s] = smem_desc(tile + s * slot_bytes, 16, 1024, kLayoutSW128);     // L, K-major
+      d_v[s] = smem_desc(tile + s * slot_bytes, kAtom, 1024, kLayoutSW128);  // L as V^T, MN-major
+      d_hi[s] = smem_desc(hi_base + s * hi_step, 16, 1024, kLayoutSW128);    // P hi, K-major
+    }
+    const int ksteps = W / 16;
+    bool ok = nh == 0 || wait_or_fail(qready, 0u, p.wait_ns, failed);
+    int ns = 0, npv = 0;
+    uint64_t t0 = global_timer_ns();
+    uint32_t spins = 0;
+    while (ok && npv < nh) {
+      bool progressed = false;
+      if (ns < nh && ns <= npv + 1 && mbar_try_wait(&full[ns & 1], (ns >> 1) & 1)) {
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const int s = ns & 1;
+        for (int k = 0; k < ksteps; ++k) {
+          const uint64_t at = ((k >> 2) * kAtom + (k & 3) * 32) >> 4;
+          mma_bf16(tmem + kKeys * s, d_q + at, d_l[s] + at, idesc_s, k != 0 ? 1u : 0u);
+        }
+        mma_commit(&sfull[s]);
+        ++ns;
+        progressed = true;
+      }
+      if (npv < ns && mbar_try_wait(pready, npv & 1)) {
+        tc_fence_after();
+        const int s = npv & 1;
+        for (int part = 0; part < 2; ++part) {
+          const uint64_t b = part ? d_hi[s] : d_lo;
+          for (int mb = 0; mb < lay.nmb; ++mb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16(tmem + 2 * kKeys + mb * kHeads, d_v[s] + ((2 * mb * kAtom + k * 2048) >> 4),
+                       b + (k * 32 >> 4), idesc_pv, (npv > 0 || part || k) ? 1u : 0u);
+          mma_commit(part ? &empty[s] : lofree);
+        }
+        ++npv;
+        progressed = true;
+      }
+      if (progressed) {
+        t0 = global_timer_ns();
+        spins = 0;
+      } else if (++spins >= 64) {
+        spins = 0;
+        if (*failed) ok = false;
+        else if (global_timer_ns() - t0 > p.wait_ns) {
+          *failed = 1u;
+          ok = false;
+        }
       }
     }
-    __syncthreads();
-    for (int k = 0; k < kKeys; ++k) {
-      if (rowi[k] < 0) continue;  // the same for every thread
-      float2 v[kMaxPairs];
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < kMaxPairs; ++i) {
-        const int c = lane + 32 * i;
-        v[i] = c < pairs ? __half22float2(tile[k][c]) : make_float2(0.f, 0.f);
-        dot += q[i].x * v[i].x + q[i].y * v[i].y;
+    if (*failed) {
+      mma_commit(bar_drain);  // fires once every MMA issued above has completed
+      mbar_wait(bar_drain, 0u, kDrainLimitNs);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool bad = *failed != 0u;
+  if (bad && tid == 0) report(p.status, kErrTimeout, (kKernMla4 << 24) | 1u);
+  const bool have_o = !bad && nh > 0;
+  if (bad && tid < kHeads) {  // whatever the softmax warps left
+    mfin[tid] = -INFINITY;
+    lfin[tid] = 0.f;
+  }
+  if (bad) __syncthreads();
+  // output, or the split's partial result: units of 32 latent columns (the
+  // warp's lane quadrant) x 32 heads, 128-byte rows per store
+  if (warp < kMmaWarp && (have_o || p.nsplit == 1)) {
+    const int q4 = warp & 3;
+    for (int u = warp >> 2; u < 2 * lay.nmb; u += kMmaWarp / 4) {
+      const int mb = u >> 1, hb = 32 * (u & 1);
+      if (hb >= p.H) continue;
+      uint32_t v[32];
+      if (have_o) {
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + 2 * kKeys + 32 * u, v);
+        tmem_ld_wait();
       }
+      const int c = mb * 128 + q4 * 32 + lane;
+      if (c < R) {
+        float *dst = p.nsplit == 1
+                         ? p.out + (static_cast<int64_t>(row) * p.H + hb) * R + c
+                         : p.part_o + ((static_cast<int64_t>(row) * p.nsplit + split) * p.H + hb) * R + c;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      const float z = dot * two_e[k] * p.scale;
-      const float mn = fmaxf(m, z), a = expf(m - mn), w = expf(z - mn);
-      m = mn;
-      l = l * a + w;
-      const float wt = w * two_e[k];
-#pragma unroll
-      for (int i = 0; i < kMaxPairs; ++i) {
-        acc[i].x = acc[i].x * a + wt * v[i].x;
-        acc[i].y = acc[i].y * a + wt * v[i].y;
+        for (int i = 0; i < 32; ++i) {
+          if (hb + i >= p.H) break;
+          float o = have_o ? __uint_as_float(v[i]) : 0.f;
+          if (p.nsplit == 1) {
+            const float l = lfin[hb + i];
+            o = l > 0.f ? o / l : (l == l ? 0.f : l);  // a NaN stays one
+          }
+          dst[static_cast<int64_t>(i) * R] = o;
+        }
       }
     }
   }
-  if (h >= p.H) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  float *out = p.out + (static_cast<int64_t>(r) * p.H + h) * p.R;
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int c = 2 * (lane + 32 * i);
-    if (c < p.R) {
-      out[c] = acc[i].x * inv;
-      out[c + 1] = acc[i].y * inv;
+  if (tid < p.H) {
+    if (p.nsplit == 1) {
+      const float l = lfin[tid];
+      p.lse[static_cast<int64_t>(row) * p.H + tid] =
+          l > 0.f ? (mfin[tid] + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+    } else {
+      float *ml = p.part_ml + (static_cast<int64_t>(row) * p.nsplit + split) * 2 * p.H;
+      ml[tid] = mfin[tid];
+      ml[p.H + tid] = lfin[tid];
     }
   }
-  if (lane == 0) p.lse[static_cast<int64_t>(r) * p.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+// Combine the split partials of one (row, head):
+//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  lse = (M + log2 L) ln 2
+// One CTA per (row, head), a thread per two columns; the splits' weights meet
+// in shared memory first.  A split without keys has l = 0 and no O.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) mla4_merge_kernel(const Mla4Params p) {
+  __shared__ float wt[kMaxSplits];
+  __shared__ float tot[2];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = lane_id();
+  const float *ml = p.part_ml + static_cast<int64_t>(row) * p.nsplit * 2 * p.H;
+  if (tid < 32) {
+    float M = -INFINITY;
+    for (int s = lane; s < p.nsplit; s += 32) M = fmaxf(M, ml[s * 2 * p.H + h]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int s = lane; s < p.nsplit; s += 32) {
+      const float m = ml[s * 2 * p.H + h], l = ml[s * 2 * p.H + p.H + h];
+      const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+      wt[s] = w;
+      L += w == 0.f ? 0.f : w * l;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) {
+      tot[0] = M;
+      tot[1] = L;
+    }
+  }
+  __syncthreads();
+  const float L = tot[1], il = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+  const int64_t stride = static_cast<int64_t>(p.H) * p.R;
+  const float *po = p.part_o + static_cast<int64_t>(row) * p.nsplit * stride + static_cast<int64_t>(h) * p.R;
+  float *out = p.out + (static_cast<int64_t>(row) * p.H + h) * p.R;
+  const int c = 2 * tid;
+  if (c < p.R) {
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float w = wt[s];
+      if (w != 0.f) {
+        const float2 v = *reinterpret_cast<const float2 *>(po + s * stride + c);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+      }
+    }
+    out[c] = acc.x * il;
+    out[c + 1] = acc.y * il;
+  }
+  if (tid == 0)
+    p.lse[static_cast<int64_t>(row) * p.H + h] =
+        L > 0.f ? (tot[0] + log2f(L)) * kLn2 : (L == L ? -INFINITY : L);
+}
+
+// Splits of a row: while rows leave SMs idle, as many CTAs per row as fit one
+// wave, one slot each at least.
+int plan_splits(int n_q, int topk) {
+  const int nh = (topk + kKeys - 1) / kKeys;
+  const int want = std::min(kMaxSplits, device_sm_count()) / std::max(1, n_q);
+  const int ns = std::max(1, std::min(want, nh));
+  const int per = (nh + ns - 1) / ns;
+  return (nh + per - 1) / per;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+// O^T partials, at H = 64: the size does not depend on the call's head count
+size_t part_o_bytes(int n_q, int ns, int R) {
+  return align256(static_cast<size_t>(n_q) * ns * kHeads * R * 4);
 }
 
 }  // namespace
 
-size_t mla4_scratch_bytes(int, int, int) { return 0; }
+size_t mla4_scratch_bytes(int n_q, int topk, int R) {
+  const int ns = plan_splits(n_q, topk);
+  if (ns == 1) return 0;
+  return part_o_bytes(n_q, ns, R) + align256(static_cast<size_t>(n_q) * ns * 2 * kHeads * 4);
+}
 
 dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
+  const int W = a.R + a.P;
+  const size_t smem = 1024 + layout_of(a.R, W).bytes;
+  if (smem > device_max_smem_optin()) return DSA_ERR_UNSUPPORTED;
+  if (func_attr_once(reinterpret_cast<const void *>(mla4_kernel),
+                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                     static_cast<int>(device_max_smem_optin())) != cudaSuccess)
+    return DSA_ERR_CUDA;
   Mla4Params p;
   p.q = a.q;
   p.latent = a.latent;
@@ -136,17 +722,33 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   p.idx = a.idx;
   p.out = a.out;
   p.lse = a.lse;
+  p.n_q = a.n_q;
   p.H = a.H;
   p.R = a.R;
-  p.W = a.R + a.P;
+  p.W = W;
   p.topk = a.topk;
-  p.scale = a.scale;
+  p.nsplit = plan_splits(a.n_q, a.topk);
+  p.part_o = nullptr;
+  p.part_ml = nullptr;
+  if (p.nsplit > 1) {
+    if (a.scratch == nullptr || a.scratch_bytes < mla4_scratch_bytes(a.n_q, a.topk, a.R))
+      return DSA_ERR_WORKSPACE;
+    p.part_o = static_cast<float *>(a.scratch);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(a.scratch) +
+                                          part_o_bytes(a.n_q, p.nsplit, a.R));
+  }
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.wait_ns = wait_limit_ns();
+  p.debug_stall = debug_stall() == static_cast<int>(kKernMla4) ? 1 : 0;
   p.status = a.status;
-  const dim3 grid(static_cast<unsigned>(a.n_q),
-                  static_cast<unsigned>((a.H + kHeadsPerCta - 1) / kHeadsPerCta));
-  return launch_pdl(mla4_simple_kernel, grid, dim3(kThreads), 0, stream, 1, p) == cudaSuccess
-             ? DSA_OK
-             : DSA_ERR_CUDA;
+  if (launch_pdl(mla4_kernel, dim3(static_cast<unsigned>(p.nsplit), static_cast<unsigned>(a.n_q)),
+                 dim3(kThreads), smem, stream, 1u, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  if (p.nsplit > 1 &&
+      launch_pdl(mla4_merge_kernel, dim3(static_cast<unsigned>(a.n_q), static_cast<unsigned>(a.H)),
+                 dim3(kMergeThreads), 0, stream, 1u, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
 }
 
 }  // namespace dsa

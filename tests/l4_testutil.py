@@ -91,5 +91,17 @@ def attention_bounds(q, L, R, scale, p):
     acc = (K / 8 + 64) * U
     mag = np.abs(L[:, :R])
     out = (p * rel) @ mag + (p * rel).sum(1, keepdims=True) * (p @ mag) + 2 * acc * (p @ mag)
+    # The weights w_j = p_j 2^e_j (up to a factor) reach the tensor cores as
+    # fp16 pairs scaled so that the largest is at least 2^6: fp16 ends in steps
+    # of 2^-24, so no w_j is off by less than 2^-25 / 2^6 = 2^-31 of the largest
+    # (a column that the large weights multiply by zero shows it).  Token j's
+    # row enters as L_j 2^-e_j, and a row's largest magnitude lies in
+    # (1250, 2688] 2^e: above half of 2688 2^e, less the scale's and the code's
+    # rounding of at most 1/16 of it.
+    big = np.abs(L).max(1)
+    live = big > 0
+    if live.any():
+        top = (p[:, live] * big[live]).max(1, keepdims=True) / 1250
+        out = out + 2.0 ** -31 * top * ((mag[live] * (2688 / big[live])[:, None]).sum(0))
     lse = (p * d).sum(1) * 2 + acc + 2.0 ** -20 + 64 * U  # |lse| below 64 in these tests
     return out + 1e-30, lse
