@@ -27,8 +27,7 @@
 //                widened, its PV product as soon as its weights are written
 // Two slots of the tile ring; S is double-buffered in tensor memory, so S of
 // one slot runs under the softmax of the other, and widening under both
-// products.  P hi goes over the slot's own atom that only S reads (the rope
-// atom at R = 512), P lo into one buffer that the PV product reads first.
+// products.
 //
 // A row split over several CTAs leaves (m, l, O) partials in global scratch
 // (they stay in L2) and a merge kernel combines them.
@@ -71,23 +70,36 @@ struct Mla4Params {
   DevStatus *status;
 };
 
+// Shared memory: the 2 nmb atoms of slot 0 that PV reads, then three atoms
+// [hi 0 | lo | hi 1], then those of slot 1, the query tile, barriers.  A slot's
+// atom 2 nmb, where it has one (columns that only S reads), lies in its hi
+// atom, which P hi overwrites once S is done with it.  With hi and lo side by
+// side, either slot's weights are one operand of 128 columns (hi | lo, or
+// lo | hi): a wide block of O^T takes both terms in one instruction, at 64
+// cycles against 2 x 48 (measured), and keeps their sums apart until the end.
 struct Layout {
-  int nQ, nmb, nL;    // query atoms, 128-column blocks of O^T, atoms per slot
-  int hi_atom;        // the slot's atom that P hi overlays, -1: buffers of its own
-  uint32_t off_q, off_hi, off_lo, off_misc, bytes;
+  int nQ, nmb;        // query atoms, 128-column blocks of O^T
+  int wide;           // blocks whose two terms accumulate side by side
+  uint32_t off_p, off_tile1, off_q, off_misc, bytes;
 };
+constexpr int kWideCols = 128;  // tensor memory columns of a wide block, against 64
 __host__ __device__ inline Layout layout_of(int R, int W) {
   Layout l;
   l.nQ = (W + 63) / 64;
   l.nmb = (R + 127) / 128;
-  l.nL = l.nQ > 2 * l.nmb ? l.nQ : 2 * l.nmb;
-  l.hi_atom = l.nL > 2 * l.nmb ? 2 * l.nmb : -1;
-  l.off_q = 2u * l.nL * kAtom;
-  l.off_hi = l.off_q + static_cast<uint32_t>(l.nQ) * kAtom;
-  l.off_lo = l.off_hi + (l.hi_atom < 0 ? 2u * kAtom : 0u);
-  l.off_misc = l.off_lo + kAtom;
+  // 512 columns: two S buffers of 64, then the blocks
+  const int spare = (512 - 2 * kKeys) / kHeads - l.nmb;
+  l.wide = l.nmb < spare ? l.nmb : spare;
+  l.off_p = 2u * l.nmb * kAtom;
+  l.off_tile1 = l.off_p + 3u * kAtom;
+  l.off_q = l.off_tile1 + 2u * l.nmb * kAtom;
+  l.off_misc = l.off_q + static_cast<uint32_t>(l.nQ) * kAtom;
   l.bytes = l.off_misc + kMisc;
   return l;
+}
+// tensor memory column of 128-column block mb of O^T
+__host__ __device__ inline int block_col(const Layout &l, int mb) {
+  return 2 * kKeys + (mb < l.wide ? mb * kWideCols : l.wide * kWideCols + (mb - l.wide) * kHeads);
 }
 
 // barrier over `n` threads that also returns whether any of them passed true
@@ -105,6 +117,20 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool v) {
 }
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// whether the phase with the given parity has completed, without waiting:
+// mbarrier.try_wait may suspend the thread for a while, which would keep the
+// MMA warp from the other product it could issue
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
 }
 // bounded wait that also gives up as soon as another role has failed
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
@@ -125,6 +151,27 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uin
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D (+)= A . B^T, fp16 operands, issued by one lane of a converged warp
+__device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// one lane's commit: arrives once every MMA that lane issued has completed
+// (the same lane is elected each time)
+__device__ __forceinline__ void commit_elect(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
 }
 // 16 lanes x 64 columns: thread t gets columns 8 i + 2 (t % 4) + {0, 1} of lane
 // t / 4 in r[4 i], r[4 i + 1] and of lane t / 4 + 8 in r[4 i + 2], r[4 i + 3]
@@ -184,10 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
                                               ~static_cast<uintptr_t>(1023));
   const int W = p.W, R = p.R;
   const Layout lay = layout_of(R, W);
-  const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q, lo_buf = tile + lay.off_lo;
-  const uint32_t slot_bytes = static_cast<uint32_t>(lay.nL) * kAtom;
-  const uint32_t hi_base = lay.hi_atom >= 0 ? tile + lay.hi_atom * kAtom : tile + lay.off_hi;
-  const uint32_t hi_step = lay.hi_atom >= 0 ? slot_bytes : kAtom;
+  const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q;
+  const uint32_t hi_base = tile + lay.off_p, lo_buf = hi_base + kAtom;  // hi of slot s: + 2 s atoms
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
   uint64_t *full = bars;        // [2] slot widened (one arrive per widening warp)
   uint64_t *empty = bars + 2;   // [2] PV of the slot completed (MMA commit)
@@ -203,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   float *qmax = reinterpret_cast<float *>(bars + 14);   // [4]
   float *alpha = qmax + 4;                              // [64]
   float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);  // [2][64] (2^e, e); (0, -inf): unused
-  float *mfin = reinterpret_cast<float *>(smem + lay.off_lo);  // [64], [64]: after the loop
+  float *mfin = reinterpret_cast<float *>(smem + lay.off_p + kAtom);  // [64], [64]: after the loop
   float *lfin = mfin + kHeads;
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
@@ -212,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   const int row = p.rows.causal ? p.n_q - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
 
   // tensor memory: S of slot s at columns 64 s, O^T from column 128
+  const int o_cols = block_col(lay, lay.nmb) - 2 * kKeys;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < static_cast<uint32_t>(2 * kKeys + lay.nmb * kHeads)) tmem_cols <<= 1;
+  while (tmem_cols < static_cast<uint32_t>(2 * kKeys + o_cols)) tmem_cols <<= 1;
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&full[s], kWideWarps);
@@ -369,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         bar_sync(1, 32 * kSoftWarps);
         tc_fence_after();
         if (alive)
-          for (int u = 0; u < 2 * lay.nmb; ++u) {
+          for (int u = 0; u < o_cols / 32; ++u) {
             const uint32_t ta = tmem + lane_off + 2 * kKeys + 32 * u;
             uint32_t o[32];
             tmem_ld_32x32b_x32(ta, o);
@@ -387,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       const float f1 = (m1 == -INFINITY ? 0.f : m1) - kWeightLog2;
       float s0 = 0.f, s1 = 0.f;
       uint32_t lw0[8], lw1[8];
-      const uint32_t hb = hi_base + s * hi_step;
+      const uint32_t hb = hi_base + 2 * s * kAtom;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float wa0 = ex2(__uint_as_float(v[4 * i]) - f0), wb0 = ex2(__uint_as_float(v[4 * i + 1]) - f0);
@@ -439,11 +485,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     const int g = warp - kSoftWarps, r8 = lane & 7, sub = lane >> 3;
     const int nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
     const int32_t *idx = p.idx + static_cast<int64_t>(row) * p.topk;
-    auto resolve = [&](int j) -> int {
-      const int place = (h_begin + j) * kKeys + 8 * g + r8;
-      if (j >= nh || place >= nsel) return -1;
-      return l4_pool_row(p.rows, row, idx[place], limit, sub == 0 ? p.status : nullptr, kKernMla4,
-                         place);
+    // A place's position, its page and its row's bytes are three dependent
+    // loads; each is issued one slot ahead of the next, so that none is waited
+    // for here.  place_of: -1 past the selection, and for positions outside the
+    // context, which are reported; row_of: -1 for those and for bad pages.
+    DevStatus *status = sub == 0 ? p.status : nullptr;
+    const int32_t *table = p.rows.block_table +
+                           (p.rows.causal ? 0 : static_cast<int64_t>(row) * p.rows.max_pages);
+    const int first = h_begin * kKeys + 8 * g + r8;
+    auto place_of = [&](int j) -> int {
+      const int place = first + j * kKeys;
+      return j < nh && place < nsel ? idx[place] : -1;
+    };
+    auto page_of = [&](int j, int &pos) -> int {
+      if (pos >= limit) {
+        report(status, kErrBadIndex, (kKernMla4 << 24) | ((first + j * kKeys) & 0xFFFF));
+        pos = -1;
+      }
+      return pos >= 0 ? table[pos / kPageSize] : -1;
+    };
+    auto row_of = [&](int j, int pos, int page) -> int {
+      if (pos < 0) return -1;
+      if (page < 0 || page >= p.rows.num_pages) {
+        report(status, kErrBadPage, (kKernMla4 << 24) | ((first + j * kKeys) & 0xFFFF));
+        return -1;
+      }
+      return page * kPageSize + pos % kPageSize;
     };
     uint4 code[kMaxUnits];
     uint32_t sc[kMaxUnits], eb = 127u;
@@ -461,13 +528,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       }
       if (sub == 0 && phys >= 0) eb = src[W / 2 + nb];
     };
-    int phys = resolve(0);
+    int pos1 = place_of(0), pos2 = place_of(1);
+    int page1 = page_of(0, pos1);
+    int phys = row_of(0, pos1, page1);
     load(phys);
-    int phys_next = resolve(1);
+    pos1 = pos2;
+    page1 = page_of(1, pos1);
+    pos2 = place_of(2);
     for (int j = 0; j < nh; ++j) {
       const int s = j & 1;
       if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
-      const uint32_t base = tile + s * slot_bytes + (8 * g + r8) * 128;
+      const uint32_t base = tile + (s ? lay.off_tile1 : 0u) + (8 * g + r8) * 128;
+      const uint32_t base_p = hi_base + 2 * s * kAtom + (8 * g + r8) * 128;
 #pragma unroll
       for (int i = 0; i < kMaxUnits; ++i) {
         const int u = sub + 4 * i;
@@ -486,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
               h[q] = *reinterpret_cast<const uint32_t *>(&x);
             }
             const uint32_t ch = static_cast<uint32_t>((4 * (u & 1) + t) ^ r8) << 4;
-            sts_v4(base + (u >> 1) * kAtom + ch, h[0], h[1], h[2], h[3]);
+            const int a = u >> 1;
+            sts_v4((a < 2 * lay.nmb ? base + a * kAtom : base_p) + ch, h[0], h[1], h[2], h[3]);
           }
         }
       }
@@ -498,53 +571,74 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
-      phys = phys_next;
+      phys = row_of(j + 1, pos1, page1);
       load(phys);
-      phys_next = resolve(j + 2);
+      pos1 = pos2;
+      page1 = page_of(j + 2, pos1);
+      pos2 = place_of(j + 3);
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------- MMA issue
+    // The whole warp runs this, so that the descriptors are computed once per
+    // warp (in uniform registers); each instruction goes out from one lane.
+    // With a single thread in the branch an instruction took 110 cycles to
+    // issue, against 45 to 64 to run.
     const uint32_t idesc_s = idesc_f16_f32(kHeads, kKeys, 0);
+    const uint32_t idesc_wide = idesc_f16_f32(128, kWideCols, 1);
     const uint32_t idesc_pv = idesc_f16_f32(128, kHeads, 1);
-    const uint64_t d_q = smem_desc(qs, 16, 1024, kLayoutSW128);
-    const uint64_t d_lo = smem_desc(lo_buf, 16, 1024, kLayoutSW128);
-    uint64_t d_l[2], d_v[2], d_hi[2];
-    for (int s = 0; s < 2; ++s) {
-      d_l[s] = smem_desc(tile + s * slot_bytes, 16, 1024, kLayoutSW128);     // L, K-major
-      d_v[s] = smem_desc(tile + s * slot_bytes, kAtom, 1024, kLayoutSW128);  // L as V^T, MN-major
-      d_hi[s] = smem_desc(hi_base + s * hi_step, 16, 1024, kLayoutSW128);    // P hi, K-major
-    }
-    const int ksteps = W / 16;
+    const int ksteps = W / 16, vsteps = 8 * lay.nmb;  // K steps of S; those of atoms that PV reads too
     bool ok = nh == 0 || wait_or_fail(qready, 0u, p.wait_ns, failed);
     int ns = 0, npv = 0;
     uint64_t t0 = global_timer_ns();
     uint32_t spins = 0;
     while (ok && npv < nh) {
       bool progressed = false;
-      if (ns < nh && ns <= npv + 1 && mbar_try_wait(&full[ns & 1], (ns >> 1) & 1)) {
+      if (ns < nh && ns <= npv + 1 && mbar_test(&full[ns & 1], (ns >> 1) & 1)) {
         fence_proxy_async_smem();
         tc_fence_after();
         const int s = ns & 1;
-        for (int k = 0; k < ksteps; ++k) {
+        const uint32_t d = tmem + kKeys * s;
+        const uint64_t d_l = smem_desc(tile + (s ? lay.off_tile1 : 0u), 16, 1024, kLayoutSW128);
+        const uint64_t d_p = smem_desc(hi_base + 2 * s * kAtom, 16, 1024, kLayoutSW128);
+        const uint64_t d_q = smem_desc(qs, 16, 1024, kLayoutSW128);
+#pragma unroll 4
+        for (int k = 0; k < min(ksteps, vsteps); ++k) {
           const uint64_t at = ((k >> 2) * kAtom + (k & 3) * 32) >> 4;
-          mma_bf16(tmem + kKeys * s, d_q + at, d_l[s] + at, idesc_s, k != 0 ? 1u : 0u);
+          mma_f16_elect(d, d_q + at, d_l + at, idesc_s, k != 0 ? 1u : 0u);
         }
-        mma_commit(&sfull[s]);
+#pragma unroll 4
+        for (int k = vsteps; k < ksteps; ++k)
+          mma_f16_elect(d, d_q + (((k >> 2) * kAtom + (k & 3) * 32) >> 4), d_p + ((k & 3) * 32 >> 4),
+                        idesc_s, 1u);
+        commit_elect(&sfull[s]);
         ++ns;
         progressed = true;
       }
-      if (npv < ns && mbar_try_wait(pready, npv & 1)) {
+      if (npv < ns && mbar_test(pready, npv & 1)) {
         tc_fence_after();
         const int s = npv & 1;
-        for (int part = 0; part < 2; ++part) {
-          const uint64_t b = part ? d_hi[s] : d_lo;
-          for (int mb = 0; mb < lay.nmb; ++mb)
+        const uint32_t more = npv > 0 ? 1u : 0u;
+        const uint64_t d_v = smem_desc(tile + (s ? lay.off_tile1 : 0u), kAtom, 1024, kLayoutSW128);
+        const uint64_t d_both = smem_desc(hi_base + s * kAtom, 16, 1024, kLayoutSW128);
+        const uint64_t d_hi = smem_desc(hi_base + 2 * s * kAtom, 16, 1024, kLayoutSW128);
+        const uint64_t d_lo = smem_desc(lo_buf, 16, 1024, kLayoutSW128);
+        for (int mb = 0; mb < lay.wide; ++mb)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16(tmem + 2 * kKeys + mb * kHeads, d_v[s] + ((2 * mb * kAtom + k * 2048) >> 4),
-                       b + (k * 32 >> 4), idesc_pv, (npv > 0 || part || k) ? 1u : 0u);
-          mma_commit(part ? &empty[s] : lofree);
-        }
+          for (int k = 0; k < 4; ++k)
+            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+                          d_both + (k * 32 >> 4), idesc_wide, k ? 1u : more);
+        for (int mb = lay.wide; mb < lay.nmb; ++mb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+                          d_lo + (k * 32 >> 4), idesc_pv, k ? 1u : more);
+        commit_elect(lofree);
+        for (int mb = lay.wide; mb < lay.nmb; ++mb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+                          d_hi + (k * 32 >> 4), idesc_pv, 1u);
+        commit_elect(&empty[s]);
         ++npv;
         progressed = true;
       }
@@ -561,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       }
     }
     if (*failed) {
-      mma_commit(bar_drain);  // fires once every MMA issued above has completed
+      commit_elect(bar_drain);  // fires once every MMA issued above has completed
       mbar_wait(bar_drain, 0u, kDrainLimitNs);
     }
   }
@@ -586,8 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       if (hb >= p.H) continue;
       uint32_t v[32];
       if (have_o) {
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + 2 * kKeys + 32 * u, v);
+        const uint32_t ta = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + block_col(lay, mb) + hb;
+        tmem_ld_32x32b_x32(ta, v);
         tmem_ld_wait();
+        if (mb < lay.wide) {
+          uint32_t w[32];
+          tmem_ld_32x32b_x32(ta + kHeads, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+        }
       }
       const int c = mb * 128 + q4 * 32 + lane;
       if (c < R) {
