@@ -58,6 +58,12 @@ __device__ __forceinline__ __half2 e4m3_to_half2(uint32_t byte) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
   return *reinterpret_cast<const __half2 *>(&h);
 }
+// two E4M3 bytes as an fp16 pair (low byte first), exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 
 // the row's power of two from its exponent byte (clamped to the format's range)

@@ -18,12 +18,13 @@
 // row that puts its largest magnitude in [2^14, 2^15).
 //
 // One CTA per SM takes a contiguous run of 64-key slots of one query row:
-//   warps 0-3    query tile; softmax of each slot (warp w: heads 16 w ..),
+//   warps 0-3    softmax of each slot (warp w: heads 16 w ..),
 //                the rare rescale of O
-//   warps 4-11   widening: warp 4 + g decodes rows 8 g .. 8 g + 7 of a slot
-//                from registers, where the next slot's bytes are already
-//                being loaded
-//   warp 12      one thread issues the MMAs: S of a slot as soon as it is
+//   (both kinds load the query tile first)
+//   warps 4-12   widening: decode a slot from registers, into which the next
+//                slot's bytes are loaded as soon as they are free
+//   warp 14      turns the selected positions into pool rows, ahead of them
+//   warp 13      issues the MMAs: S of a slot as soon as it is
 //                widened, its PV product as soon as its weights are written
 // Two slots of the tile ring; S is double-buffered in tensor memory, so S of
 // one slot runs under the softmax of the other, and widening under both
@@ -40,18 +41,22 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 416;
+constexpr int kThreads = 480;
 constexpr int kSoftWarps = 4;
-constexpr int kWideWarps = 8;
+constexpr int kWideWarps = 9;
 constexpr int kMmaWarp = kSoftWarps + kWideWarps;
+constexpr int kRowWarp = kMmaWarp + 1;
+constexpr int kOutWarps = 8;           // warps that write the output, two per tensor memory quadrant
 constexpr int kHeads = 64;
 constexpr int kKeys = 64;              // keys per slot
 constexpr int kAtom = kKeys * 128;     // bytes of a 64-column atom of 64 rows (tile or query)
-constexpr int kMaxUnits = 5;           // 16-byte code units per lane: 18 at W = 576, over 4 lanes
+constexpr int kWorkers = 32 * (kSoftWarps + kWideWarps);
+constexpr int kMaxQ = (kHeads * 72 + kWorkers - 1) / kWorkers;  // 16-byte query pieces per worker at W = 576
+constexpr int kTasks = 4;              // widening tasks per warp and slot: 36 over 9 warps
 constexpr int kWeightLog2 = 6;         // weights enter the tensor cores scaled by 2^6
 constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceeded by 2^8
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kMisc = 1536;
+constexpr int kMisc = 2048;
 constexpr int kMaxSplits = 148;
 
 struct Mla4Params {
@@ -64,6 +69,7 @@ struct Mla4Params {
   float *part_o;   // [n_q, nsplit, H, R]      (nsplit > 1)
   float *part_ml;  // [n_q, nsplit, 2, H]
   int n_q, H, R, W, topk, nsplit;
+  uint32_t cpr_inv;  // ceil(2^20 / (W / 8)): t / (W / 8) = t * cpr_inv >> 20 for t < 64 * 72
   float scale_log2;
   uint64_t wait_ns;
   int debug_stall;
@@ -135,7 +141,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 // bounded wait that also gives up as soon as another role has failed
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
                                              volatile uint32_t *failed) {
-  if (mbar_try_wait(bar, parity)) return true;
+  // the first tries do without the timer, whose reading takes hundreds of cycles
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
 #pragma unroll 1
@@ -201,13 +210,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -219,6 +221,28 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// loads of 16 and 8 bits into a 32-bit register as they are: a conversion after
+// the load would be waited for at once, and these are issued a slot ahead
+__device__ __forceinline__ uint32_t ldg_u16(const void *a) {
+  uint32_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_u8(const void *a) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
+// w[t] = w[(t + n) % 4]
+__device__ __forceinline__ void rotate4(uint32_t (&w)[4], int n) {
+  const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+  const bool one = n & 1, two = n & 2;
+  const uint32_t x0 = one ? b : a, x1 = one ? c : b, x2 = one ? d : c, x3 = one ? a : d;
+  w[0] = two ? x2 : x0;
+  w[1] = two ? x3 : x1;
+  w[2] = two ? x0 : x2;
+  w[3] = two ? x1 : x3;
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -242,12 +266,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   uint64_t *qready = bars + 8;  // query tile written (one arrive per softmax warp)
   uint64_t *bar_drain = bars + 9;
   uint64_t *bar_stall = bars + 10;
+  uint64_t *rowfull = bars + 11;  // [2] the slot's pool rows known (row warp)
+  uint64_t *rowfree = bars + 13;  // [2] and read (one arrive per widening warp)
   // [0] tensor memory base, [1] failed
-  volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 12);
+  volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 16);
   volatile uint32_t *failed = misc + 1;
-  float *qmax = reinterpret_cast<float *>(bars + 14);   // [4]
-  float *alpha = qmax + 4;                              // [64]
-  float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);  // [2][64] (2^e, e); (0, -inf): unused
+  float *qmax = reinterpret_cast<float *>(bars + 18);   // [13], padded to 16
+  float *alpha = qmax + 16;                             // [64]
+  float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);    // [2][64] (2^e, e); (0, -inf): unused
+  int *rowi = reinterpret_cast<int *>(keys + 2 * kKeys);        // [2][64] pool row, -1: none
   float *mfin = reinterpret_cast<float *>(smem + lay.off_p + kAtom);  // [64], [64]: after the loop
   float *lfin = mfin + kHeads;
 
@@ -265,10 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       mbar_init(&full[s], kWideWarps);
       mbar_init(&empty[s], 1);
       mbar_init(&sfull[s], 1);
+      mbar_init(&rowfull[s], 1);
+      mbar_init(&rowfree[s], kWideWarps);
     }
     mbar_init(pready, kSoftWarps);
     mbar_init(lofree, 1);
-    mbar_init(qready, kSoftWarps);
+    mbar_init(qready, kSoftWarps + kWideWarps);
     mbar_init(bar_drain, 1);
     mbar_init(bar_stall, 1);
     *failed = 0u;
@@ -299,61 +328,109 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   const int h_begin = min(nh_row, split * per);
   const int nh = min(nh_row, h_begin + per) - h_begin;
 
-  if (warp < kSoftWarps) {
-    // ------------------------------------------------- query tile, softmax
-    // the 64-head query tile (heads >= H zero), 128B-swizzled, K-major; first
-    // as bf16, then scaled to fp16 in place by the threads that loaded it
-    const int cpr = W / 8;  // 16-byte pieces per row
-    if (nh > 0) {
-      const uint16_t *qrow = p.q + static_cast<int64_t>(row) * p.H * W;
-      for (int h = warp; h < kHeads; h += kSoftWarps)
-        for (int c = lane; c < cpr; c += 32) {
-          const bool ok = h < p.H;
-          cp_async_16(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4),
-                      ok ? qrow + h * W + c * 8 : p.q, ok ? 16u : 0u);
-        }
-      cp_async_commit();
-      cp_async_wait_all();
+  // Widening: the bytes of a slot's 64 rows come in 36 tasks of 32 16-byte
+  // code units, four per warp.  Task t < 32: units 0-15 of rows 2 t and 2 t + 1,
+  // sixteen lanes side by side per row (with four lanes per row the loads took
+  // twice the cache lines each, and the load path, which the tile's stores
+  // share, was the limit); task 32 + t: units 16 and 17 of rows 16 t .. 16 t + 15.
+  const int g = warp - kSoftWarps, nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
+  auto task_row = [&](int i) {
+    const int t = g + kWideWarps * i;
+    return t < 32 ? 2 * t + (lane >> 4) : 16 * (t - 32) + (lane >> 1);
+  };
+  auto task_unit = [&](int i) { return g + kWideWarps * i < 32 ? (lane & 15) : 16 + (lane & 1); };
+  uint4 code[kTasks];
+  uint32_t sc[kTasks], eb[kTasks];  // the unit's two block scales, the row's exponent byte
+  uint32_t have = 0u;               // bit i: task i's row exists
+  // The next slot's bytes, into registers.  Every lane loads, from the pool's
+  // first row and the row's first unit where it has none of its own (a branch
+  // around the loads cost more than they do); the scales are dropped later.
+  auto load_rows = [&](int j) -> bool {
+    const int s = j & 1;
+    if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) return false;
+    int r[kTasks];
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) r[i] = rowi[s * kKeys + task_row(i)];
+    have = 0u;
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) {
+      const int u = task_unit(i) < units ? task_unit(i) : 0;
+      have |= (r[i] >= 0 ? 1u : 0u) << i;
+      const uint8_t *src = p.latent + static_cast<int64_t>(max(r[i], 0)) * rb;
+      code[i] = *reinterpret_cast<const uint4 *>(src + 16 * u);
+      sc[i] = ldg_u16(src + W / 2 + 2 * u);
+      eb[i] = ldg_u8(src + W / 2 + nb);
     }
-    float zscale;  // logit units: log2(e) * scale / the query's power of two
-    {
-      float mx = 0.f;
-      if (nh > 0)
-        for (int h = warp; h < kHeads; h += kSoftWarps)
-          for (int c = lane; c < cpr; c += 32) {
-            const uint4 v = lds_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&rowfree[s]);
+    return true;
+  };
+
+  // The 64-head query tile (heads >= H zero), 128B-swizzled, K-major: every
+  // worker thread holds up to twelve 16-byte pieces in registers while the
+  // row's largest magnitude is found, then stores them scaled to fp16
+  const int cpr = W / 8;  // 16-byte pieces per head
+  uint4 qv[kMaxQ];
+  if (warp < kMmaWarp && nh > 0) {
+    const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(row) * p.H * W);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
-                                   fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
-          }
+    for (int i = 0; i < kMaxQ; ++i) {
+      const int t = tid + kWorkers * i;
+      qv[i] = t < p.H * cpr ? qrow[t] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (warp < kMmaWarp) {
+    float mx = 0.f;
+    if (nh > 0) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) qmax[warp] = mx;
-      bar_sync(1, 32 * kSoftWarps);
-      mx = fmaxf(fmaxf(qmax[0], qmax[1]), fmaxf(qmax[2], qmax[3]));
-      const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-      const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
-      const float f = pow2i(k);
-      zscale = p.scale_log2 * pow2i(-k);
-      if (nh > 0)
-        for (int h = warp; h < kHeads; h += kSoftWarps)
-          for (int c = lane; c < cpr; c += 32) {
-            const uint32_t a = qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4);
-            const uint4 v = lds_v4(a);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < kMaxQ; ++i) {
+        const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
+                               fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) qmax[warp] = mx;
+  }
+  __syncthreads();
+  float zscale;  // logit units: log2(e) * scale / the query's power of two
+  {
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMmaWarp; ++i) mx = fmaxf(mx, qmax[i]);
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+    const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
+    const float f = pow2i(k);
+    zscale = p.scale_log2 * pow2i(-k);
+    if (warp < kMmaWarp) {
+      if (nh > 0) {
+#pragma unroll
+        for (int i = 0; i < kMaxQ; ++i) {
+          const int t = tid + kWorkers * i;
+          if (t < kHeads * cpr) {
+            const int h = static_cast<int>((static_cast<uint32_t>(t) * p.cpr_inv) >> 20);  // t / cpr
+            const int c = t - h * cpr;
+            const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
             uint32_t o[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              o[t] = pack_f16(__uint_as_float(w[t] << 16) * f,
-                              __uint_as_float(w[t] & 0xFFFF0000u) * f);
-            sts_v4(a, o[0], o[1], o[2], o[3]);
+            for (int x = 0; x < 4; ++x)
+              o[x] = pack_f16(__uint_as_float(w[x] << 16) * f,
+                              __uint_as_float(w[x] & 0xFFFF0000u) * f);
+            sts_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
           }
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
     }
+  }
+
+  if (warp < kSoftWarps) {
+    // --------------------------------------------------------------- softmax
     const int r0 = lane >> 2, c2 = 2 * (lane & 3);
     const int h0 = 16 * warp + r0, h1 = h0 + 8;  // this thread's two heads
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
@@ -370,14 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       uint32_t v[32];
       tmem_ld_16x256b_x8(tmem + lane_off + kKeys * s, v);
       tmem_ld_wait();
-      float inv[16];  // 2^-e of the 16 keys
       float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 k = *reinterpret_cast<const float4 *>(&keys[s * kKeys + 8 * i + c2]);
         const float ka = k.x * zscale, kb = k.z * zscale;
-        inv[2 * i] = __uint_as_float((254u << 23) - __float_as_uint(k.x));
-        inv[2 * i + 1] = __uint_as_float((254u << 23) - __float_as_uint(k.z));
         const float a0 = fmaf(__uint_as_float(v[4 * i]), ka, k.y);
         const float b0 = fmaf(__uint_as_float(v[4 * i + 1]), kb, k.w);
         const float a1 = fmaf(__uint_as_float(v[4 * i + 2]), ka, k.y);
@@ -438,8 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       for (int i = 0; i < 8; ++i) {
         const float wa0 = ex2(__uint_as_float(v[4 * i]) - f0), wb0 = ex2(__uint_as_float(v[4 * i + 1]) - f0);
         const float wa1 = ex2(__uint_as_float(v[4 * i + 2]) - f1), wb1 = ex2(__uint_as_float(v[4 * i + 3]) - f1);
-        s0 = fmaf(wb0, inv[2 * i + 1], fmaf(wa0, inv[2 * i], s0));
-        s1 = fmaf(wb1, inv[2 * i + 1], fmaf(wa1, inv[2 * i], s1));
+        const float4 k = *reinterpret_cast<const float4 *>(&keys[s * kKeys + 8 * i + c2]);
+        const float ia = __uint_as_float((254u << 23) - __float_as_uint(k.x));  // 2^-e
+        const float ib = __uint_as_float((254u << 23) - __float_as_uint(k.z));
+        s0 = fmaf(wb0, ib, fmaf(wa0, ia, s0));
+        s1 = fmaf(wb1, ib, fmaf(wa1, ia, s1));
         const uint32_t hi0 = pack_f16(wa0, wb0), hi1 = pack_f16(wa1, wb1);
         const float2 g0 = __half22float2(as_half2(hi0)), g1 = __half22float2(as_half2(hi1));
         lw0[i] = pack_f16(wa0 - g0.x, wb0 - g0.y);
@@ -481,174 +558,166 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     }
   } else if (warp < kMmaWarp) {
     // -------------------------------------------------------------- widening
-    // lane: row r8 of the warp's eight, every fourth 16-byte code unit from sub
-    const int g = warp - kSoftWarps, r8 = lane & 7, sub = lane >> 3;
-    const int nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
-    const int32_t *idx = p.idx + static_cast<int64_t>(row) * p.topk;
-    // A place's position, its page and its row's bytes are three dependent
-    // loads; each is issued one slot ahead of the next, so that none is waited
-    // for here.  place_of: -1 past the selection, and for positions outside the
-    // context, which are reported; row_of: -1 for those and for bad pages.
-    DevStatus *status = sub == 0 ? p.status : nullptr;
-    const int32_t *table = p.rows.block_table +
-                           (p.rows.causal ? 0 : static_cast<int64_t>(row) * p.rows.max_pages);
-    const int first = h_begin * kKeys + 8 * g + r8;
-    auto place_of = [&](int j) -> int {
-      const int place = first + j * kKeys;
-      return j < nh && place < nsel ? idx[place] : -1;
-    };
-    auto page_of = [&](int j, int &pos) -> int {
-      if (pos >= limit) {
-        report(status, kErrBadIndex, (kKernMla4 << 24) | ((first + j * kKeys) & 0xFFFF));
-        pos = -1;
-      }
-      return pos >= 0 ? table[pos / kPageSize] : -1;
-    };
-    auto row_of = [&](int j, int pos, int page) -> int {
-      if (pos < 0) return -1;
-      if (page < 0 || page >= p.rows.num_pages) {
-        report(status, kErrBadPage, (kKernMla4 << 24) | ((first + j * kKeys) & 0xFFFF));
-        return -1;
-      }
-      return page * kPageSize + pos % kPageSize;
-    };
-    uint4 code[kMaxUnits];
-    uint32_t sc[kMaxUnits], eb = 127u;
-    auto load = [&](int phys) {
-      const uint8_t *src = p.latent + static_cast<int64_t>(phys < 0 ? 0 : phys) * rb;
-#pragma unroll
-      for (int i = 0; i < kMaxUnits; ++i) {
-        const int u = sub + 4 * i;
-        code[i] = make_uint4(0u, 0u, 0u, 0u);
-        sc[i] = 0u;
-        if (phys >= 0 && u < units) {
-          code[i] = *reinterpret_cast<const uint4 *>(src + 16 * u);
-          sc[i] = *reinterpret_cast<const uint16_t *>(src + W / 2 + 2 * u);
-        }
-      }
-      if (sub == 0 && phys >= 0) eb = src[W / 2 + nb];
-    };
-    int pos1 = place_of(0), pos2 = place_of(1);
-    int page1 = page_of(0, pos1);
-    int phys = row_of(0, pos1, page1);
-    load(phys);
-    pos1 = pos2;
-    page1 = page_of(1, pos1);
-    pos2 = place_of(2);
-    for (int j = 0; j < nh; ++j) {
+    bool loaded = nh > 0 && load_rows(0);
+    for (int j = 0; j < nh && loaded; ++j) {
       const int s = j & 1;
       if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
-      const uint32_t base = tile + (s ? lay.off_tile1 : 0u) + (8 * g + r8) * 128;
-      const uint32_t base_p = hi_base + 2 * s * kAtom + (8 * g + r8) * 128;
 #pragma unroll
-      for (int i = 0; i < kMaxUnits; ++i) {
-        const int u = sub + 4 * i;
-        if (u < units) {
-          const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-          const __half2 s_lo = e4m3_to_half2(sc[i]), s_hi = e4m3_to_half2(sc[i] >> 8);
+      for (int i = 0; i < kTasks; ++i) {
+        const int u = task_unit(i), r = task_row(i), a = u >> 1;
+        const bool live = (have >> i) & 1u;
+        const uint32_t dst = r * 128 + (a < 2 * lay.nmb ? tile + a * kAtom + s * lay.off_tile1
+                                                        : hi_base + 2 * s * kAtom);
+        // the four words in an order turned by the unit, so that eight
+        // neighbouring lanes store to eight different 16-byte columns
+        const int rot = a & 3;
+        const uint32_t x = (4 * (u & 1)) ^ (r & 7);
+        uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        rotate4(w, rot);
+        const uint32_t both = e4m3x2_to_f16x2(live ? sc[i] : 0u);  // no row: zeros
+        const __half2 s_lo = as_half2(__byte_perm(both, 0u, 0x1010)), s_hi = as_half2(__byte_perm(both, 0u, 0x3232));
+        // at W = 16 (mod 32) the last unit's second block is no column
+        const int words = u >= units ? 0 : (2 * u + 1 < nb ? 4 : 2);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (t >= 2 && 2 * u + 1 >= nb) break;  // W = 16 (mod 32): the unit's second block is no column
-            uint32_t h[4];
-            e2m1x8_to_f16x2(w[t], h);
-            const __half2 sv = t < 2 ? s_lo : s_hi;
+        for (int t = 0; t < 4; ++t) {
+          const int tw = (t + rot) & 3;  // the word, 8 columns
+          uint32_t h[4];
+          e2m1x8_to_f16x2(w[t], h);
+          const __half2 sv = tw < 2 ? s_lo : s_hi;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const __half2 x = __hmul2(as_half2(h[q]), sv);
-              h[q] = *reinterpret_cast<const uint32_t *>(&x);
-            }
-            const uint32_t ch = static_cast<uint32_t>((4 * (u & 1) + t) ^ r8) << 4;
-            const int a = u >> 1;
-            sts_v4((a < 2 * lay.nmb ? base + a * kAtom : base_p) + ch, h[0], h[1], h[2], h[3]);
+          for (int q = 0; q < 4; ++q) {
+            const __half2 y = __hmul2(as_half2(h[q]), sv);
+            h[q] = *reinterpret_cast<const uint32_t *>(&y);
           }
+          if (tw < words) sts_v4(dst + ((x ^ tw) << 4), h[0], h[1], h[2], h[3]);
         }
-      }
-      if (sub == 0) {
-        const int e = l4_exponent(eb);
-        keys[s * kKeys + 8 * g + r8] =
-            phys >= 0 ? make_float2(pow2i(e), static_cast<float>(e)) : make_float2(0.f, -INFINITY);
+        if (u == 0) {
+          const int e = l4_exponent(eb[i]);
+          keys[s * kKeys + r] = live ? make_float2(pow2i(e), static_cast<float>(e))
+                                     : make_float2(0.f, -INFINITY);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
-      phys = row_of(j + 1, pos1, page1);
-      load(phys);
-      pos1 = pos2;
-      page1 = page_of(j + 2, pos1);
-      pos2 = place_of(j + 3);
+      if (j + 1 < nh) loaded = load_rows(j + 1);
+    }
+  } else if (warp == kRowWarp) {
+    // -------------------------------------------------------------- pool rows
+    // Places 2 lane and 2 lane + 1 of each slot: position, page, pool row; the
+    // next slot's positions are loaded before this one's pages are waited for.
+    // Positions outside the context and bad pages are dropped and reported.
+    const int32_t *idx = p.idx + static_cast<int64_t>(row) * p.topk;
+    auto position = [&](int j, int x) -> int {
+      const int place = (h_begin + j) * kKeys + 2 * lane + x;
+      return j < nh && place < nsel ? idx[place] : -1;
+    };
+    int pos[2] = {position(0, 0), position(0, 1)};
+    for (int j = 0; j < nh; ++j) {
+      const int s = j & 1;
+      const int next[2] = {position(j + 1, 0), position(j + 1, 1)};
+      int r[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        r[x] = l4_pool_row(p.rows, row, pos[x], limit, p.status, kKernMla4,
+                           (h_begin + j) * kKeys + 2 * lane + x);
+      if (j >= 2 && !wait_or_fail(&rowfree[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+      *reinterpret_cast<int2 *>(&rowi[s * kKeys + 2 * lane]) = make_int2(r[0], r[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rowfull[s]);
+      pos[0] = next[0];
+      pos[1] = next[1];
     }
   } else {
     // ------------------------------------------------------------- MMA issue
-    // The whole warp runs this, so that the descriptors are computed once per
-    // warp (in uniform registers); each instruction goes out from one lane.
-    // With a single thread in the branch an instruction took 110 cycles to
-    // issue, against 45 to 64 to run.
+    // The whole warp runs this and branches on votes, so that the descriptors
+    // are computed once per warp, in uniform registers; each instruction goes
+    // out from one lane.  (From a single-thread branch an instruction took 110
+    // cycles to issue, against the 45 to 64 it runs.)
     const uint32_t idesc_s = idesc_f16_f32(kHeads, kKeys, 0);
     const uint32_t idesc_wide = idesc_f16_f32(128, kWideCols, 1);
     const uint32_t idesc_pv = idesc_f16_f32(128, kHeads, 1);
-    const int ksteps = W / 16, vsteps = 8 * lay.nmb;  // K steps of S; those of atoms that PV reads too
-    bool ok = nh == 0 || wait_or_fail(qready, 0u, p.wait_ns, failed);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tile_u = __shfl_sync(0xffffffffu, tile, 0);
+    const uint32_t p_u = tile_u + lay.off_p;
+    const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;  // of the query; K steps after them
+    const int v_atoms = 2 * lay.nmb;                                // atoms that lie in the tile
+    const int tile_atoms = min(full_atoms, v_atoms);
+    const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
+    bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
     int ns = 0, npv = 0;
-    uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     uint32_t spins = 0;
     while (ok && npv < nh) {
       bool progressed = false;
-      if (ns < nh && ns <= npv + 1 && mbar_test(&full[ns & 1], (ns >> 1) & 1)) {
+      if (ns < nh && ns <= npv + 1 &&
+          __all_sync(0xffffffffu, mbar_test(&full[ns & 1], (ns >> 1) & 1))) {
         fence_proxy_async_smem();
         tc_fence_after();
         const int s = ns & 1;
-        const uint32_t d = tmem + kKeys * s;
-        const uint64_t d_l = smem_desc(tile + (s ? lay.off_tile1 : 0u), 16, 1024, kLayoutSW128);
-        const uint64_t d_p = smem_desc(hi_base + 2 * s * kAtom, 16, 1024, kLayoutSW128);
-        const uint64_t d_q = smem_desc(qs, 16, 1024, kLayoutSW128);
+        const uint32_t d = tm + kKeys * s;
+        const uint64_t d_l = smem_desc(tile_u + s * lay.off_tile1, 16, 1024, kLayoutSW128);
+        const uint64_t d_p = smem_desc(p_u + 2 * s * kAtom, 16, 1024, kLayoutSW128);
+        // four K steps per 64-column atom; the columns that only S reads lie
+        // in the P region
 #pragma unroll 4
-        for (int k = 0; k < min(ksteps, vsteps); ++k) {
-          const uint64_t at = ((k >> 2) * kAtom + (k & 3) * 32) >> 4;
-          mma_f16_elect(d, d_q + at, d_l + at, idesc_s, k != 0 ? 1u : 0u);
-        }
-#pragma unroll 4
-        for (int k = vsteps; k < ksteps; ++k)
-          mma_f16_elect(d, d_q + (((k >> 2) * kAtom + (k & 3) * 32) >> 4), d_p + ((k & 3) * 32 >> 4),
-                        idesc_s, 1u);
+        for (int a = 0; a < tile_atoms; ++a)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_elect(d, d_q + ((a * kAtom + k * 32) >> 4), d_l + ((a * kAtom + k * 32) >> 4),
+                          idesc_s, (a | k) != 0 ? 1u : 0u);
+        for (int a = tile_atoms; a < full_atoms; ++a)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_elect(d, d_q + ((a * kAtom + k * 32) >> 4), d_p + (k * 32 >> 4), idesc_s, 1u);
+        for (int k = 0; k < tail; ++k)
+          mma_f16_elect(d, d_q + ((full_atoms * kAtom + k * 32) >> 4),
+                        (full_atoms < v_atoms ? d_l + ((full_atoms * kAtom + k * 32) >> 4)
+                                              : d_p + (k * 32 >> 4)),
+                        idesc_s, (full_atoms | k) != 0 ? 1u : 0u);
         commit_elect(&sfull[s]);
         ++ns;
         progressed = true;
       }
-      if (npv < ns && mbar_test(pready, npv & 1)) {
+      if (npv < ns && __all_sync(0xffffffffu, mbar_test(pready, npv & 1))) {
         tc_fence_after();
         const int s = npv & 1;
         const uint32_t more = npv > 0 ? 1u : 0u;
-        const uint64_t d_v = smem_desc(tile + (s ? lay.off_tile1 : 0u), kAtom, 1024, kLayoutSW128);
-        const uint64_t d_both = smem_desc(hi_base + s * kAtom, 16, 1024, kLayoutSW128);
-        const uint64_t d_hi = smem_desc(hi_base + 2 * s * kAtom, 16, 1024, kLayoutSW128);
-        const uint64_t d_lo = smem_desc(lo_buf, 16, 1024, kLayoutSW128);
+        const uint64_t d_v = smem_desc(tile_u + s * lay.off_tile1, kAtom, 1024, kLayoutSW128);
+        const uint64_t d_both = smem_desc(p_u + s * kAtom, 16, 1024, kLayoutSW128);
+        const uint64_t d_hi = smem_desc(p_u + 2 * s * kAtom, 16, 1024, kLayoutSW128);
+        const uint64_t d_lo = smem_desc(p_u + kAtom, 16, 1024, kLayoutSW128);
+        const uint32_t o = tm + 2 * kKeys, on = o + lay.wide * kWideCols;  // wide, narrow blocks
+        const uint64_t d_vn = d_v + ((lay.wide * 2 * kAtom) >> 4);
+        const int narrow = lay.nmb - lay.wide;
+#pragma unroll 2
         for (int mb = 0; mb < lay.wide; ++mb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+            mma_f16_elect(o + mb * kWideCols, d_v + ((2 * mb * kAtom + k * 2048) >> 4),
                           d_both + (k * 32 >> 4), idesc_wide, k ? 1u : more);
-        for (int mb = lay.wide; mb < lay.nmb; ++mb)
+#pragma unroll 2
+        for (int mb = 0; mb < narrow; ++mb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+            mma_f16_elect(on + mb * kHeads, d_vn + ((2 * mb * kAtom + k * 2048) >> 4),
                           d_lo + (k * 32 >> 4), idesc_pv, k ? 1u : more);
         commit_elect(lofree);
-        for (int mb = lay.wide; mb < lay.nmb; ++mb)
+#pragma unroll 2
+        for (int mb = 0; mb < narrow; ++mb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_elect(tmem + block_col(lay, mb), d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+            mma_f16_elect(on + mb * kHeads, d_vn + ((2 * mb * kAtom + k * 2048) >> 4),
                           d_hi + (k * 32 >> 4), idesc_pv, 1u);
         commit_elect(&empty[s]);
         ++npv;
         progressed = true;
       }
       if (progressed) {
-        t0 = global_timer_ns();
         spins = 0;
-      } else if (++spins >= 64) {
-        spins = 0;
-        if (*failed) ok = false;
-        else if (global_timer_ns() - t0 > p.wait_ns) {
+      } else if (++spins % 64 == 0) {
+        const uint64_t now = global_timer_ns();
+        if (spins == 64) t0 = now;
+        if (__any_sync(0xffffffffu, *failed != 0u || now - t0 > p.wait_ns)) {
           *failed = 1u;
           ok = false;
         }
@@ -673,9 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   if (bad) __syncthreads();
   // output, or the split's partial result: units of 32 latent columns (the
   // warp's lane quadrant) x 32 heads, 128-byte rows per store
-  if (warp < kMmaWarp && (have_o || p.nsplit == 1)) {
+  if (warp < kOutWarps && (have_o || p.nsplit == 1)) {
     const int q4 = warp & 3;
-    for (int u = warp >> 2; u < 2 * lay.nmb; u += kMmaWarp / 4) {
+    for (int u = warp >> 2; u < 2 * lay.nmb; u += kOutWarps / 4) {
       const int mb = u >> 1, hb = 32 * (u & 1);
       if (hb >= p.H) continue;
       uint32_t v[32];
@@ -831,6 +900,7 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   p.W = W;
   p.topk = a.topk;
   p.nsplit = plan_splits(a.n_q, a.topk);
+  p.cpr_inv = ((1u << 20) + W / 8 - 1) / (W / 8);
   p.part_o = nullptr;
   p.part_ml = nullptr;
   if (p.nsplit > 1) {
