@@ -21,10 +21,10 @@
 //   warps 0-3    softmax of each slot (warp w: heads 16 w ..),
 //                the rare rescale of O
 //   (both kinds load the query tile first)
-//   warps 4-12   widening: decode a slot from registers, into which the next
+//   warps 4-11, 14   widening: decode a slot from registers, into which the next
 //                slot's bytes are loaded as soon as they are free
-//   warp 14      turns the selected positions into pool rows, ahead of them
-//   warp 13      issues the MMAs: S of a slot as soon as it is
+//   warp 13      turns the selected positions into pool rows, ahead of them
+//   warp 12      issues the MMAs: S of a slot as soon as it is
 //                widened, its PV product as soon as its weights are written
 // Two slots of the tile ring; S is double-buffered in tensor memory, so S of
 // one slot runs under the softmax of the other, and widening under both
@@ -41,12 +41,14 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 480;
-constexpr int kSoftWarps = 4;
-constexpr int kWideWarps = 9;
-constexpr int kMmaWarp = kSoftWarps + kWideWarps;
-constexpr int kRowWarp = kMmaWarp + 1;
-constexpr int kOutWarps = 8;           // warps that write the output, two per tensor memory quadrant
+constexpr int kThreads = 512;
+constexpr int kSoftWarps = 4;            // warps 0-3
+constexpr int kWideWarps = 9;            // warps 4-11 and 14
+constexpr int kMmaWarp = 12, kRowWarp = 13, kLastWideWarp = 14;
+constexpr int kOutWarps = 12;            // warps that read O out, three per tensor memory quadrant
+// Registers: 128 a thread at launch (512 threads); the softmax warps take what
+// the others give up, 128 x 168 + 384 x 112 = 64,512 of the 65,536
+constexpr int kSoftRegs = 168, kOtherRegs = 112;
 constexpr int kHeads = 64;
 constexpr int kKeys = 64;              // keys per slot
 constexpr int kAtom = kKeys * 128;     // bytes of a 64-column atom of 64 rows (tile or query)
@@ -157,6 +159,14 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uin
     }
   }
 }
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -234,6 +244,9 @@ __device__ __forceinline__ uint32_t ldg_u8(const void *a) {
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(a));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void *a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
 // w[t] = w[(t + n) % 4]
 __device__ __forceinline__ void rotate4(uint32_t (&w)[4], int n) {
   const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   float *alpha = qmax + 16;                             // [64]
   float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);    // [2][64] (2^e, e); (0, -inf): unused
   int *rowi = reinterpret_cast<int *>(keys + 2 * kKeys);        // [2][64] pool row, -1: none
-  float *mfin = reinterpret_cast<float *>(smem + lay.off_p + kAtom);  // [64], [64]: after the loop
+  float *mfin = reinterpret_cast<float *>(keys);                // [64], [64]: after the loop
   float *lfin = mfin + kHeads;
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
@@ -333,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   // sixteen lanes side by side per row (with four lanes per row the loads took
   // twice the cache lines each, and the load path, which the tile's stores
   // share, was the limit); task 32 + t: units 16 and 17 of rows 16 t .. 16 t + 15.
-  const int g = warp - kSoftWarps, nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
+  const bool worker = warp < kMmaWarp || warp == kLastWideWarp;
+  const int g = warp == kLastWideWarp ? kWideWarps - 1 : warp - kSoftWarps, nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
   auto task_row = [&](int i) {
     const int t = g + kWideWarps * i;
     return t < 32 ? 2 * t + (lane >> 4) : 16 * (t - 32) + (lane >> 1);
@@ -369,17 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   // The 64-head query tile (heads >= H zero), 128B-swizzled, K-major: every
   // worker thread holds up to twelve 16-byte pieces in registers while the
   // row's largest magnitude is found, then stores them scaled to fp16
-  const int cpr = W / 8;  // 16-byte pieces per head
-  uint4 qv[kMaxQ];
-  if (warp < kMmaWarp && nh > 0) {
-    const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(row) * p.H * W);
+  float zscale = 0.f;  // logit units: log2(e) * scale / the query's power of two
+  if (worker) {
+    const int cpr = W / 8;  // 16-byte pieces per head
+    const int wtid = warp == kLastWideWarp ? kWorkers - 32 + lane : tid;
+    uint4 qv[kMaxQ];
+    if (nh > 0) {
+      const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(row) * p.H * W);
 #pragma unroll
-    for (int i = 0; i < kMaxQ; ++i) {
-      const int t = tid + kWorkers * i;
-      qv[i] = t < p.H * cpr ? qrow[t] : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kMaxQ; ++i) {
+        const int t = wtid + kWorkers * i;
+        qv[i] = t < p.H * cpr ? qrow[t] : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
-  }
-  if (warp < kMmaWarp) {
     float mx = 0.f;
     if (nh > 0) {
 #pragma unroll
@@ -393,41 +409,36 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) qmax[warp] = mx;
-  }
-  __syncthreads();
-  float zscale;  // logit units: log2(e) * scale / the query's power of two
-  {
-    float mx = 0.f;
+    if (lane == 0) qmax[wtid >> 5] = mx;
+    bar_sync(2, kWorkers);
 #pragma unroll
-    for (int i = 0; i < kMmaWarp; ++i) mx = fmaxf(mx, qmax[i]);
+    for (int i = 0; i < kSoftWarps + kWideWarps; ++i) mx = fmaxf(mx, qmax[i]);
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
     const float f = pow2i(k);
     zscale = p.scale_log2 * pow2i(-k);
-    if (warp < kMmaWarp) {
-      if (nh > 0) {
+    if (nh > 0) {
 #pragma unroll
-        for (int i = 0; i < kMaxQ; ++i) {
-          const int t = tid + kWorkers * i;
-          if (t < kHeads * cpr) {
-            const int h = static_cast<int>((static_cast<uint32_t>(t) * p.cpr_inv) >> 20);  // t / cpr
-            const int c = t - h * cpr;
-            const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-            uint32_t o[4];
+      for (int i = 0; i < kMaxQ; ++i) {
+        const int t = wtid + kWorkers * i;
+        if (t < kHeads * cpr) {
+          const int h = static_cast<int>((static_cast<uint32_t>(t) * p.cpr_inv) >> 20);  // t / cpr
+          const int c = t - h * cpr;
+          const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+          uint32_t o[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              o[x] = pack_f16(__uint_as_float(w[x] << 16) * f,
-                              __uint_as_float(w[x] & 0xFFFF0000u) * f);
-            sts_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
-          }
+          for (int x = 0; x < 4; ++x)
+            o[x] = pack_f16(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
+          sts_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qready);
   }
+  if (warp < kSoftWarps) regs_inc<kSoftRegs>();
+  else regs_dec<kOtherRegs>();
 
   if (warp < kSoftWarps) {
     // --------------------------------------------------------------- softmax
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       lfin[h0] = good ? l0 : 0.f;
       lfin[h1] = good ? l1 : 0.f;
     }
-  } else if (warp < kMmaWarp) {
+  } else if (worker) {
     // -------------------------------------------------------------- widening
     bool loaded = nh > 0 && load_rows(0);
     for (int j = 0; j < nh && loaded; ++j) {
@@ -622,13 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         r[x] = l4_pool_row(p.rows, row, pos[x], limit, p.status, kKernMla4,
                            (h_begin + j) * kKeys + 2 * lane + x);
       if (j >= 2 && !wait_or_fail(&rowfree[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+      // into L2 ahead of the widening warps' loads: a row is 336 bytes at
+      // W = 576, four lines at most
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (r[x] >= 0) {
+          const uint8_t *src = p.latent + static_cast<int64_t>(r[x]) * rb;
+          for (int b = 0; b < rb; b += 128) prefetch_l2(src + b);
+          prefetch_l2(src + rb - 1);
+        }
       *reinterpret_cast<int2 *>(&rowi[s * kKeys + 2 * lane]) = make_int2(r[0], r[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&rowfull[s]);
       pos[0] = next[0];
       pos[1] = next[1];
     }
-  } else {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
     // The whole warp runs this and branches on votes, so that the descriptors
     // are computed once per warp, in uniform registers; each instruction goes
@@ -740,8 +760,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     lfin[tid] = 0.f;
   }
   if (bad) __syncthreads();
-  // output, or the split's partial result: units of 32 latent columns (the
-  // warp's lane quadrant) x 32 heads, 128-byte rows per store
+  // Output, or the split's partial result: units of 32 latent columns (the
+  // warp's lane quadrant) x 32 heads, 128 bytes per head and store.  (Staging
+  // the block in shared memory for one bulk copy took longer.)
+  float *dst = p.nsplit == 1 ? p.out + static_cast<int64_t>(row) * p.H * R
+                             : p.part_o + (static_cast<int64_t>(row) * p.nsplit + split) * p.H * R;
+  if (p.nsplit == 1) {  // what O is multiplied by: 1 / l, 0 for an empty row; a NaN stays one
+    if (tid < kHeads) {
+      const float l = lfin[tid];
+      alpha[tid] = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    }
+    __syncthreads();
+  }
   if (warp < kOutWarps && (have_o || p.nsplit == 1)) {
     const int q4 = warp & 3;
     for (int u = warp >> 2; u < 2 * lay.nmb; u += kOutWarps / 4) {
@@ -751,7 +781,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       if (have_o) {
         const uint32_t ta = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + block_col(lay, mb) + hb;
         tmem_ld_32x32b_x32(ta, v);
-        tmem_ld_wait();
         if (mb < lay.wide) {
           uint32_t w[32];
           tmem_ld_32x32b_x32(ta + kHeads, w);
@@ -759,22 +788,19 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+        } else {
+          tmem_ld_wait();
         }
       }
-      const int c = mb * 128 + q4 * 32 + lane;
+      const int c = mb * 128 + q4 * 32 + lane, left = p.H - hb;
       if (c < R) {
-        float *dst = p.nsplit == 1
-                         ? p.out + (static_cast<int64_t>(row) * p.H + hb) * R + c
-                         : p.part_o + ((static_cast<int64_t>(row) * p.nsplit + split) * p.H + hb) * R + c;
+        float *at = dst + static_cast<int64_t>(hb) * R + c;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          if (hb + i >= p.H) break;
           float o = have_o ? __uint_as_float(v[i]) : 0.f;
-          if (p.nsplit == 1) {
-            const float l = lfin[hb + i];
-            o = l > 0.f ? o / l : (l == l ? 0.f : l);  // a NaN stays one
-          }
-          dst[static_cast<int64_t>(i) * R] = o;
+          if (p.nsplit == 1) o *= alpha[hb + i];
+          if (i < left) *at = o;
+          at += R;
         }
       }
     }
@@ -801,15 +827,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
 
 // Combine the split partials of one (row, head):
 //   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  lse = (M + log2 L) ln 2
-// One CTA per (row, head), a thread per two columns; the splits' weights meet
-// in shared memory first.  A split without keys has l = 0 and no O.
-constexpr int kMergeThreads = 256;
-__global__ void __launch_bounds__(kMergeThreads) mla4_merge_kernel(const Mla4Params p) {
+// One CTA per (row, head): kGroups groups of 128 threads take every kGroups-th
+// split, a thread four columns.  The loads of O (kMergeBatch splits per group
+// at once) are in flight while one warp forms the splits' weights, so the
+// kernel waits on memory once for up to kGroups * kMergeBatch splits; few
+// splits come with many rows and take one group, so that more CTAs fit an SM.
+// A split without keys has l = 0 and wrote no O: what its place holds is read
+// and dropped.
+constexpr int kMergeBatch = 8;
+template <int kGroups>
+__global__ void __launch_bounds__(128 * kGroups) mla4_merge_kernel(const Mla4Params p) {
   __shared__ float wt[kMaxSplits];
   __shared__ float tot[2];
+  __shared__ float4 part[kGroups][128];
   griddep_wait();
   griddep_launch_dependents();
   const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = lane_id();
+  const int grp = tid >> 7, c = 4 * (tid & 127);
+  const int64_t stride = static_cast<int64_t>(p.H) * p.R;
+  const float *po = p.part_o + static_cast<int64_t>(row) * p.nsplit * stride + static_cast<int64_t>(h) * p.R;
+  float4 v[kMergeBatch];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kMergeBatch; ++i) {
+      const int s = s0 + kGroups * i;
+      v[i] = s < p.nsplit && c < p.R ? *reinterpret_cast<const float4 *>(po + s * stride + c)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(grp);
   const float *ml = p.part_ml + static_cast<int64_t>(row) * p.nsplit * 2 * p.H;
   if (tid < 32) {
     float M = -INFINITY;
@@ -831,24 +877,42 @@ __global__ void __launch_bounds__(kMergeThreads) mla4_merge_kernel(const Mla4Par
     }
   }
   __syncthreads();
-  const float L = tot[1], il = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
-  const int64_t stride = static_cast<int64_t>(p.H) * p.R;
-  const float *po = p.part_o + static_cast<int64_t>(row) * p.nsplit * stride + static_cast<int64_t>(h) * p.R;
-  float *out = p.out + (static_cast<int64_t>(row) * p.H + h) * p.R;
-  const int c = 2 * tid;
-  if (c < p.R) {
-    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int s = 0; s < p.nsplit; ++s) {
-      const float w = wt[s];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = grp; s0 < p.nsplit; s0 += kGroups * kMergeBatch) {
+    if (s0 != grp) load(s0);
+#pragma unroll
+    for (int i = 0; i < kMergeBatch; ++i) {
+      const int s = s0 + kGroups * i;
+      const float w = s < p.nsplit ? wt[s] : 0.f;
       if (w != 0.f) {
-        const float2 v = *reinterpret_cast<const float2 *>(po + s * stride + c);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
+        acc.x = fmaf(w, v[i].x, acc.x);
+        acc.y = fmaf(w, v[i].y, acc.y);
+        acc.z = fmaf(w, v[i].z, acc.z);
+        acc.w = fmaf(w, v[i].w, acc.w);
       }
     }
-    out[c] = acc.x * il;
-    out[c + 1] = acc.y * il;
+  }
+  if constexpr (kGroups > 1) {
+    part[grp][tid & 127] = acc;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 b = part[g][tid];
+        acc.x += b.x;
+        acc.y += b.y;
+        acc.z += b.z;
+        acc.w += b.w;
+      }
+    }
+  }
+  const float L = tot[1], il = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+  if (grp == 0 && c < p.R) {
+    float *out = p.out + (static_cast<int64_t>(row) * p.H + h) * p.R + c;  // 4-byte aligned only
+    out[0] = acc.x * il;
+    out[1] = acc.y * il;
+    out[2] = acc.z * il;
+    out[3] = acc.w * il;
   }
   if (tid == 0)
     p.lse[static_cast<int64_t>(row) * p.H + h] =
@@ -917,11 +981,15 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   if (launch_pdl(mla4_kernel, dim3(static_cast<unsigned>(p.nsplit), static_cast<unsigned>(a.n_q)),
                  dim3(kThreads), smem, stream, 1u, p) != cudaSuccess)
     return DSA_ERR_CUDA;
-  if (p.nsplit > 1 &&
-      launch_pdl(mla4_merge_kernel, dim3(static_cast<unsigned>(a.n_q), static_cast<unsigned>(a.H)),
-                 dim3(kMergeThreads), 0, stream, 1u, p) != cudaSuccess)
-    return DSA_ERR_CUDA;
-  return DSA_OK;
+  if (p.nsplit == 1) return DSA_OK;
+  const int groups = p.nsplit > 2 * kMergeBatch ? 4 : (p.nsplit > kMergeBatch ? 2 : 1);
+  void (*merge)(const Mla4Params) = groups == 4   ? mla4_merge_kernel<4>
+                                    : groups == 2 ? mla4_merge_kernel<2>
+                                                  : mla4_merge_kernel<1>;
+  return launch_pdl(merge, dim3(static_cast<unsigned>(a.n_q), static_cast<unsigned>(a.H)),
+                    dim3(128u * groups), 0, stream, 1u, p) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // namespace dsa
