@@ -2,23 +2,25 @@
 //
 //   mass_out[b, s] = decay * mass_in[b, s] + sum_{r, h, j: idx[r,j] = s} exp(z[r,h,j] - lse[r,h])
 //
-// Two kernels.  decay_kernel writes decay * mass_in over the live positions
-// (and clears the 64-bit sums of a causal chunk).  mass_kernel recomputes the
-// logits of every kept row - one CTA of eight warps per query row, one warp
-// per kept token, the lanes over the columns - and adds the head sum.  A
+// decay_kernel writes decay * mass_in over the live positions (and clears the
+// 64-bit sums of a causal chunk).  mass_kernel recomputes the logits on tcgen05
+//   S = L . Q^T   M = 64 kept keys, N = 64 heads, K = R + P
+// over the same pipeline as the attention over a 4-bit cache, without its
+// second product: a row warp turns positions into pool rows, nine warps fill
+// one of two 64-key slots (4-bit and E4M3 rows widened to fp16, exactly; bf16
+// rows as they are), one issues the MMAs, four read S with a key per lane
+// quad, so the sum over heads stays inside a thread but for two shuffles.  A
 // decode row adds in fp32 (its positions are its own); the rows of a causal
 // chunk add to one sequence, in 64-bit fixed point so that the order does not
 // matter, and fold_kernel turns the sums into fp32.
-#include <cuda_bf16.h>
-#include <math.h>
+#include <algorithm>
 
-#include "latent4.cuh"
+#include "l4_tile.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxPairs = 9;
+constexpr int kSweep = 256;  // threads of the sweeps over positions
 constexpr double kFixedOne = 1099511627776.0;  // 2^40: a weight of 64 heads x 2^17 rows stays below 2^63
 
 struct MassParams {
@@ -32,8 +34,11 @@ struct MassParams {
   float *mass_out;
   unsigned long long *fixed;
   int64_t mass_ld;
-  int n_q, num_seqs, H, R, W, topk;
-  float scale, decay;
+  int n_q, num_seqs, H, W, topk, nsplit;
+  uint32_t cpr_inv, units_inv;  // inverses of 16-byte pieces per query head and per stored row, at 2^20
+  float scale_log2, decay;
+  uint64_t wait_ns;
+  int debug_stall;
   DevStatus *status;
 };
 
@@ -43,87 +48,397 @@ __device__ __forceinline__ int mass_len(const MassParams &p, int b) {
   return static_cast<int>(min(static_cast<int64_t>(max(0, len)), p.mass_ld));
 }
 
-__global__ void __launch_bounds__(kThreads) decay_kernel(const MassParams p) {
+__global__ void __launch_bounds__(kSweep) decay_kernel(const MassParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y, n = mass_len(p, b);
-  for (int s = blockIdx.x * kThreads + threadIdx.x; s < n; s += gridDim.x * kThreads) {
+#pragma unroll 4
+  for (int s = blockIdx.x * kSweep + threadIdx.x; s < n; s += gridDim.x * kSweep) {
     const int64_t at = b * p.mass_ld + s;
     p.mass_out[at] = p.mass_in ? p.decay * p.mass_in[at] : 0.f;
     if (p.fixed) p.fixed[s] = 0ull;
   }
 }
 
-template <int F>
-__device__ __forceinline__ float2 latent_pair(const uint8_t *row, int W, int c) {
-  if constexpr (F == kLatBf16) {
-    const uint32_t v = reinterpret_cast<const uint32_t *>(row)[c];
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-  } else if constexpr (F == kLatE4m3) {
-    return make_float2(__low2float(e4m3_to_half2(row[2 * c])), __low2float(e4m3_to_half2(row[2 * c + 1])));
-  } else {
-    uint32_t h[4];
-    e2m1x8_to_f16x2(reinterpret_cast<const uint32_t *>(row)[c / 4], h);
-    const uint32_t pair = (c & 2) ? ((c & 1) ? h[3] : h[2]) : ((c & 1) ? h[1] : h[0]);
-    return __half22float2(__hmul2(as_half2(pair), e4m3_to_half2(row[W / 2 + c / 8])));
-  }
+// one row's weight of one kept position
+__device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos, float w) {
+  if (pos < 0 || pos >= p.mass_ld) return;
+  if (p.rows.causal)
+    atomicAdd(&p.fixed[pos], static_cast<unsigned long long>(
+                                 __double2ll_rn(static_cast<double>(w) * kFixedOne)));
+  else
+    atomicAdd(&p.mass_out[static_cast<int64_t>(row) * p.mass_ld + pos], w);
 }
 
+
+// Shared memory: two slots of the tile (64 keys x W), the query tile, barriers.
+constexpr int kMisc = 1536;
+struct Layout {
+  int nQ;
+  uint32_t slot, off_q, off_misc, bytes;
+};
+__host__ __device__ inline Layout layout_of(int W) {
+  Layout l;
+  l.nQ = (W + 63) / 64;
+  l.slot = static_cast<uint32_t>(l.nQ) * kAtom;
+  l.off_q = 2u * l.slot;
+  l.off_misc = l.off_q + l.slot;
+  l.bytes = l.off_misc + kMisc;
+  return l;
+}
+// 16-byte units of a stored row's columns, and the tasks of 32 units a filling
+// warp takes per slot at W = 576
 template <int F>
-__global__ void __launch_bounds__(kThreads) mass_simple_kernel(const MassParams p) {
+__host__ __device__ constexpr int units_of(int W) {
+  return F == kLatBf16 ? W / 8 : (F == kLatE4m3 ? W / 16 : (W / kL4Block + 1) / 2);
+}
+template <int F>
+constexpr int kTasksOf = (2 * units_of<F>(576) + kWideWarps - 1) / kWideWarps;
+
+template <int F>
+__global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const int W = p.W;
+  const Layout lay = layout_of(W);
+  const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
+  uint64_t *full = bars;         // [2] slot filled (one arrive per filling warp)
+  uint64_t *empty = bars + 2;    // [2] S and key factors read (one arrive per summing warp)
+  uint64_t *sfull = bars + 4;    // [2] S in tensor memory (MMA commit)
+  uint64_t *rowfull = bars + 6;  // [2] the slot's pool rows known (row warp)
+  uint64_t *rowfree = bars + 8;  // [2] and read (one arrive per filling warp)
+  uint64_t *qready = bars + 10;
+  uint64_t *bar_drain = bars + 11;
+  uint64_t *bar_stall = bars + 12;
+  // [0] tensor memory base, [1] failed
+  volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 14);
+  volatile uint32_t *failed = misc + 1;
+  float *qmax = reinterpret_cast<float *>(bars + 16);      // [13], padded to 16
+  float *factor = qmax + 16;                               // [2][64] a key's scale, +inf: unused
+  int *rowi = reinterpret_cast<int *>(factor + 2 * kKeys);  // [2][64] pool row, -1: none
+
+  const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
+  const int split = blockIdx.x;
+  const int row = p.rows.causal ? p.n_q - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&full[s], kWideWarps);
+      mbar_init(&empty[s], kSoftWarps);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&rowfull[s], 1);
+      mbar_init(&rowfree[s], kWideWarps);
+    }
+    mbar_init(qready, kSoftWarps + kWideWarps);
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_stall, 1);
+    *failed = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(const_cast<uint32_t *>(&misc[0]), 2 * kKeys);
+    tmem_relinquish();
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.x, warp = warp_id(), lane = lane_id();
-  const int W = p.W, pairs = W / 2;
-  const int bytes = F == kLatBf16 ? 2 * W : (F == kLatE4m3 ? W : l4_row_bytes(W));
-  const int len = l4_row_len(p.rows, r), limit = l4_limit(p.rows, len);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  if (p.debug_stall) {
+    if (tid == 0 && !mbar_wait(bar_stall, 0u, p.wait_ns)) *failed = 1u;
+    __syncthreads();
+  }
+  const int len = l4_row_len(p.rows, row), limit = l4_limit(p.rows, len);
   const int nsel = max(0, min(p.topk, len));
-  for (int j = blockIdx.y * (kThreads / 32) + warp; j < nsel; j += gridDim.y * (kThreads / 32)) {
-    const int pos = p.idx[static_cast<int64_t>(r) * p.topk + j];
-    int row = -1;
-    if (lane == 0) row = l4_pool_row(p.rows, r, pos, limit, p.status, kKernMass, j);
-    row = __shfl_sync(0xffffffffu, row, 0);
-    if (row < 0 || pos >= p.mass_ld) continue;
-    const uint8_t *src = p.latent + static_cast<int64_t>(row) * bytes;
-    const float t = F == kLatL4 ? pow2i(l4_exponent(src[W / 2 + W / kL4Block]))
-                                : (F == kLatE4m3 ? p.lat_scale[row] : 1.f);
-    float2 v[kMaxPairs];
+  const int nh_row = (nsel + kKeys - 1) / kKeys;
+  const int per = (nh_row + p.nsplit - 1) / p.nsplit;
+  const int h_begin = min(nh_row, split * per);
+  const int nh = min(nh_row, h_begin + per) - h_begin;
+  const int32_t *idx = p.idx + static_cast<int64_t>(row) * p.topk;
+
+  const bool worker = warp < kMmaWarp || warp == kLastWideWarp;
+  float zscale = 0.f;
+  if (worker)
+    zscale = load_query_tile<F != kLatBf16>(p.q + static_cast<int64_t>(row) * p.H * W, qs, p.H, W,
+                                            p.cpr_inv, nh > 0,
+                                            warp == kLastWideWarp ? kWorkers - 32 + lane : tid, qmax,
+                                            qready) * p.scale_log2;
+  if (warp < kSoftWarps) regs_inc<kSoftRegs>();
+  else regs_dec<kOtherRegs>();
+
+  if (warp < kSoftWarps) {
+    // --------------------------------------------------------------- head sums
+    // lane t reads keys 16 warp + t / 4 (+ 8), heads 8 i + 2 (t % 4) + {0, 1}
+    const int k0 = 16 * warp + (lane >> 2), c2 = 2 * (lane & 3);
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    float ls[16];  // log2 units; +inf where the head adds nothing
 #pragma unroll
-    for (int i = 0; i < kMaxPairs; ++i) {
-      const int c = lane + 32 * i;
-      v[i] = c < pairs ? latent_pair<F>(src, W, c) : make_float2(0.f, 0.f);
+    for (int i = 0; i < 16; ++i) {
+      const int h = 8 * (i >> 1) + c2 + (i & 1);
+      const float l = h < p.H ? p.lse[static_cast<int64_t>(row) * p.H + h] : -INFINITY;
+      ls[i] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
     }
-    float w = 0.f;
-    for (int h = 0; h < p.H; ++h) {
-      const uint32_t *q = reinterpret_cast<const uint32_t *>(p.q + (static_cast<int64_t>(r) * p.H + h) * W);
-      float dot = 0.f;
+    auto place = [&](int j, int x) -> int {
+      const int at = (h_begin + j) * kKeys + k0 + 8 * x;
+      return j < nh && at < nsel ? idx[at] : -1;
+    };
+    int pos[2] = {place(0, 0), place(0, 1)};
+    for (int j = 0; j < nh; ++j) {
+      const int s = j & 1;
+      const uint32_t par = (j >> 1) & 1;
+      if (!wait_or_fail(&sfull[s], par, p.wait_ns, failed) ||
+          !wait_or_fail(&full[s], par, p.wait_ns, failed))
+        break;
+      const int next[2] = {place(j + 1, 0), place(j + 1, 1)};
+      tc_fence_after();
+      uint32_t v[32];
+      tmem_ld_16x256b_x8(tmem + lane_off + kKeys * s, v);
+      const float f0 = factor[s * kKeys + k0], f1 = factor[s * kKeys + k0 + 8];
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      const float t0 = f0 * zscale, t1 = f1 * zscale;
+      float w0 = 0.f, w1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < kMaxPairs; ++i) {
-        const int c = lane + 32 * i;
-        if (c < pairs)
-          dot += __uint_as_float(q[c] << 16) * v[i].x + __uint_as_float(q[c] & 0xFFFF0000u) * v[i].y;
+      for (int i = 0; i < 8; ++i) {
+        w0 += ex2(fmaf(__uint_as_float(v[4 * i]), t0, -ls[2 * i])) +
+              ex2(fmaf(__uint_as_float(v[4 * i + 1]), t0, -ls[2 * i + 1]));
+        w1 += ex2(fmaf(__uint_as_float(v[4 * i + 2]), t1, -ls[2 * i])) +
+              ex2(fmaf(__uint_as_float(v[4 * i + 3]), t1, -ls[2 * i + 1]));
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      const float lse = p.lse[static_cast<int64_t>(r) * p.H + h];
-      if (lse > -INFINITY) w += expf(dot * t * p.scale - lse);
+      for (int o = 1; o < 4; o <<= 1) {
+        w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+        w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+      }
+      if ((lane & 3) == 0) {
+        if (f0 != INFINITY) add_weight(p, row, pos[0], w0);
+        if (f1 != INFINITY) add_weight(p, row, pos[1], w1);
+      }
+      pos[0] = next[0];
+      pos[1] = next[1];
     }
-    if (lane == 0) {
-      if (p.rows.causal)
-        atomicAdd(&p.fixed[pos], static_cast<unsigned long long>(__double2ll_rn(static_cast<double>(w) * kFixedOne)));
-      else
-        atomicAdd(&p.mass_out[static_cast<int64_t>(r) * p.mass_ld + pos], w);
+  } else if (worker) {
+    // ----------------------------------------------------------------- filling
+    // A slot's 64 x units 16-byte units, 32 neighbours per task: coalesced, and
+    // eight neighbouring lanes store to eight different 16-byte columns
+    constexpr int kT = kTasksOf<F>;
+    const int g = warp == kLastWideWarp ? kWideWarps - 1 : warp - kSoftWarps;
+    const int units = units_of<F>(W), nb = W / kL4Block;
+    const int bytes = F == kLatBf16 ? 2 * W : (F == kLatE4m3 ? W : l4_row_bytes(W));
+    int r_of[kT], u_of[kT];  // row -1: no unit
+#pragma unroll
+    for (int i = 0; i < kT; ++i) {
+      const uint32_t t = static_cast<uint32_t>((g + kWideWarps * i) * 32 + lane);
+      const int r = static_cast<int>((t * p.units_inv) >> 20);
+      r_of[i] = r < kKeys ? r : -1;
+      u_of[i] = static_cast<int>(t) - r * units;
     }
+    auto set_factor = [&](int s, int r, bool live, float f) {
+      factor[s * kKeys + r] = live ? f : INFINITY;
+    };
+    if constexpr (F == kLatBf16) {
+      // straight into the tile, one slot behind the one being waited for
+      for (int j = 0; j <= nh; ++j) {
+        const int s = j & 1;
+        if (j < nh) {
+          if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) break;
+          if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+#pragma unroll
+          for (int i = 0; i < kT; ++i) {
+            if (r_of[i] < 0) continue;
+            const int r = r_of[i], u = u_of[i], at = rowi[s * kKeys + r];
+            const uint8_t *src = p.latent + static_cast<int64_t>(max(at, 0)) * bytes + 16 * u;
+            cp_async_16(tile + s * lay.slot + (u >> 3) * kAtom + r * 128 + (((u & 7) ^ (r & 7)) << 4),
+                        src, at >= 0 ? 16u : 0u);
+            if (u == 0) set_factor(s, r, at >= 0, 1.f);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rowfree[s]);
+        }
+        cp_async_commit();
+        if (j > 0) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s ^ 1]);
+        }
+      }
+      cp_async_wait_all();
+    } else {
+      uint4 data[kT];
+      uint32_t sc[kT];  // 4-bit rows: the unit's two block scales
+      float ef[kT];     // the row's factor (for unit 0)
+      uint32_t have = 0u;
+      auto load_rows = [&](int j) -> bool {
+        const int s = j & 1;
+        if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) return false;
+        have = 0u;
+#pragma unroll
+        for (int i = 0; i < kT; ++i) {
+          const int at = r_of[i] >= 0 ? rowi[s * kKeys + r_of[i]] : -1;
+          have |= (at >= 0 ? 1u : 0u) << i;
+          const int u = r_of[i] >= 0 ? u_of[i] : 0;
+          const uint8_t *src = p.latent + static_cast<int64_t>(max(at, 0)) * bytes;
+          data[i] = *reinterpret_cast<const uint4 *>(src + 16 * u);
+          if constexpr (F == kLatL4) {
+            sc[i] = ldg_u16(src + W / 2 + 2 * u);
+            ef[i] = __uint_as_float(ldg_u8(src + W / 2 + nb));
+          } else {
+            ef[i] = p.lat_scale[max(at, 0)];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rowfree[s]);
+        return true;
+      };
+      bool loaded = nh > 0 && load_rows(0);
+      for (int j = 0; j < nh && loaded; ++j) {
+        const int s = j & 1;
+        if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+#pragma unroll
+        for (int i = 0; i < kT; ++i) {
+          if (r_of[i] < 0) continue;
+          const int r = r_of[i], u = u_of[i];
+          const bool live = (have >> i) & 1u;
+          const uint32_t base = tile + s * lay.slot + r * 128;
+          uint32_t w[4] = {data[i].x, data[i].y, data[i].z, data[i].w};
+          if constexpr (F == kLatL4) {
+            const uint32_t dst = base + (u >> 1) * kAtom;
+            const int rot = (u >> 1) & 3;
+            const uint32_t x = (4 * (u & 1)) ^ (r & 7);
+            rotate4(w, rot);
+            const uint32_t both = e4m3x2_to_f16x2(live ? sc[i] : 0u);
+            const __half2 s_lo = as_half2(__byte_perm(both, 0u, 0x1010)), s_hi = as_half2(__byte_perm(both, 0u, 0x3232));
+            const int words = 2 * u + 1 < nb ? 4 : 2;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int tw = (t + rot) & 3;
+              uint32_t h[4];
+              e2m1x8_to_f16x2(w[t], h);
+              const __half2 sv = tw < 2 ? s_lo : s_hi;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const __half2 y = __hmul2(as_half2(h[q]), sv);
+                h[q] = *reinterpret_cast<const uint32_t *>(&y);
+              }
+              if (tw < words) sts_v4(dst + ((x ^ tw) << 4), h[0], h[1], h[2], h[3]);
+            }
+          } else {
+            // 16 E4M3 values: two 16-byte columns of fp16, in an order turned
+            // by the unit
+            const uint32_t dst = base + (u >> 2) * kAtom;
+            const int turn = (u >> 2) & 1;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int half = t ^ turn;
+              const uint32_t a = half ? w[2] : w[0], b = half ? w[3] : w[1];
+              const uint32_t keep = live ? 0xFFFFFFFFu : 0u;
+              sts_v4(dst + ((((2 * u + half) & 7) ^ (r & 7)) << 4), e4m3x2_to_f16x2(a & keep & 0xFFFFu),
+                     e4m3x2_to_f16x2((a & keep) >> 16), e4m3x2_to_f16x2(b & keep & 0xFFFFu),
+                     e4m3x2_to_f16x2((b & keep) >> 16));
+            }
+          }
+          if (u == 0)
+            set_factor(s, r, live, F == kLatL4 ? pow2i(l4_exponent(__float_as_uint(ef[i]))) : ef[i]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (j + 1 < nh) loaded = load_rows(j + 1);
+      }
+    }
+  } else if (warp == kRowWarp) {
+    // --------------------------------------------------------------- pool rows
+    auto position = [&](int j, int x) -> int {
+      const int at = (h_begin + j) * kKeys + 2 * lane + x;
+      return j < nh && at < nsel ? idx[at] : -1;
+    };
+    int pos[2] = {position(0, 0), position(0, 1)};
+    for (int j = 0; j < nh; ++j) {
+      const int s = j & 1;
+      const int next[2] = {position(j + 1, 0), position(j + 1, 1)};
+      int r[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        r[x] = l4_pool_row(p.rows, row, pos[x], limit, p.status, kKernMass,
+                           (h_begin + j) * kKeys + 2 * lane + x);
+      if (j >= 2 && !wait_or_fail(&rowfree[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+      *reinterpret_cast<int2 *>(&rowi[s * kKeys + 2 * lane]) = make_int2(r[0], r[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rowfull[s]);
+      pos[0] = next[0];
+      pos[1] = next[1];
+    }
+  } else if (warp == kMmaWarp) {
+    // --------------------------------------------------------------- MMA issue
+    // S = L . Q^T, M = 64 keys, N = 64 heads, K = W; the converged warp computes
+    // the descriptors in uniform registers
+    const uint32_t idesc = idesc_f16_f32(kKeys, kHeads, 0, F == kLatBf16 ? 1 : 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tile_u = __shfl_sync(0xffffffffu, tile, 0);
+    const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
+    const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;
+    bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
+    for (int j = 0; j < nh && ok; ++j) {
+      const int s = j & 1;
+      if (!__all_sync(0xffffffffu, wait_or_fail(&full[s], (j >> 1) & 1, p.wait_ns, failed))) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      const uint32_t d = tm + kKeys * s;
+      const uint64_t d_l = smem_desc(tile_u + s * lay.slot, 16, 1024, kLayoutSW128);
+#pragma unroll 3
+      for (int a = 0; a < full_atoms; ++a)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16_elect(d, d_l + ((a * kAtom + k * 32) >> 4), d_q + ((a * kAtom + k * 32) >> 4),
+                        idesc, (a | k) != 0 ? 1u : 0u);
+      for (int k = 0; k < tail; ++k)
+        mma_f16_elect(d, d_l + ((full_atoms * kAtom + k * 32) >> 4),
+                      d_q + ((full_atoms * kAtom + k * 32) >> 4), idesc, (full_atoms | k) != 0 ? 1u : 0u);
+      commit_elect(&sfull[s]);
+    }
+    if (*failed) {
+      commit_elect(bar_drain);
+      mbar_wait(bar_drain, 0u, kDrainLimitNs);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*failed && tid == 0) report(p.status, kErrTimeout, (kKernMass << 24) | 1u);
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tmem, 2 * kKeys);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) fold_kernel(const MassParams p) {
+__global__ void __launch_bounds__(kSweep) fold_kernel(const MassParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int n = mass_len(p, 0);
-  for (int s = blockIdx.x * kThreads + threadIdx.x; s < n; s += gridDim.x * kThreads)
+  for (int s = blockIdx.x * kSweep + threadIdx.x; s < n; s += gridDim.x * kSweep)
     p.mass_out[s] = static_cast<float>(static_cast<double>(p.mass_out[s]) +
                                        static_cast<double>(p.fixed[s]) * (1.0 / kFixedOne));
+}
+
+template <int F>
+dsa_status_t launch_sums(MassParams p, cudaStream_t stream) {
+  const size_t smem = 1024 + layout_of(p.W).bytes;
+  if (smem > device_max_smem_optin()) return DSA_ERR_UNSUPPORTED;
+  if (func_attr_once(reinterpret_cast<const void *>(mass_kernel<F>),
+                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                     static_cast<int>(device_max_smem_optin())) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const int units = units_of<F>(p.W);
+  p.units_inv = ((1u << 20) + units - 1) / units;
+  return launch_pdl(mass_kernel<F>, dim3(static_cast<unsigned>(p.nsplit), static_cast<unsigned>(p.n_q)),
+                    dim3(kThreads), smem, stream, 1u, p) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -147,23 +462,27 @@ dsa_status_t launch_mass(const MassLaunch &a, cudaStream_t stream) {
   p.n_q = a.n_q;
   p.num_seqs = a.num_seqs;
   p.H = a.H;
-  p.R = a.R;
   p.W = a.R + a.P;
   p.topk = a.topk;
-  p.scale = a.scale;
+  p.cpr_inv = query_pieces_inverse(p.W);
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.decay = a.decay;
+  p.wait_ns = wait_limit_ns();
+  p.debug_stall = debug_stall() == static_cast<int>(kKernMass) ? 1 : 0;
   p.status = a.status;
+  // a row's 64-key slots over as many CTAs as fit one wave
+  const int slots = (a.topk + kKeys - 1) / kKeys;
+  p.nsplit = std::max(1, std::min(slots, device_sm_count() / std::max(1, a.n_q)));
   const unsigned seqs = a.rows.causal ? 1u : static_cast<unsigned>(a.num_seqs);
-  if (launch_pdl(decay_kernel, dim3(32, seqs), dim3(kThreads), 0, stream, 1, p) != cudaSuccess)
+  const unsigned sweep = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(128, (a.mass_ld + 4 * kSweep - 1) / (4 * kSweep))));
+  if (launch_pdl(decay_kernel, dim3(sweep, seqs), dim3(kSweep), 0, stream, 1, p) != cudaSuccess)
     return DSA_ERR_CUDA;
-  const dim3 grid(static_cast<unsigned>(a.n_q), 8);
-  const cudaError_t e =
-      a.format == kLatBf16   ? launch_pdl(mass_simple_kernel<kLatBf16>, grid, dim3(kThreads), 0, stream, 1, p)
-      : a.format == kLatE4m3 ? launch_pdl(mass_simple_kernel<kLatE4m3>, grid, dim3(kThreads), 0, stream, 1, p)
-                             : launch_pdl(mass_simple_kernel<kLatL4>, grid, dim3(kThreads), 0, stream, 1, p);
-  if (e != cudaSuccess) return DSA_ERR_CUDA;
+  const dsa_status_t st = a.format == kLatBf16   ? launch_sums<kLatBf16>(p, stream)
+                          : a.format == kLatE4m3 ? launch_sums<kLatE4m3>(p, stream)
+                                                 : launch_sums<kLatL4>(p, stream);
+  if (st != DSA_OK) return st;
   if (a.rows.causal &&
-      launch_pdl(fold_kernel, dim3(32), dim3(kThreads), 0, stream, 1, p) != cudaSuccess)
+      launch_pdl(fold_kernel, dim3(sweep), dim3(kSweep), 0, stream, 1, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return DSA_OK;
 }

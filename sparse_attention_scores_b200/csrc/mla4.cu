@@ -36,24 +36,12 @@
 
 #include <algorithm>
 
-#include "latent4.cuh"
+#include "l4_tile.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kSoftWarps = 4;            // warps 0-3
-constexpr int kWideWarps = 9;            // warps 4-11 and 14
-constexpr int kMmaWarp = 12, kRowWarp = 13, kLastWideWarp = 14;
 constexpr int kOutWarps = 12;            // warps that read O out, three per tensor memory quadrant
-// Registers: 128 a thread at launch (512 threads); the softmax warps take what
-// the others give up, 128 x 168 + 384 x 112 = 64,512 of the 65,536
-constexpr int kSoftRegs = 168, kOtherRegs = 112;
-constexpr int kHeads = 64;
-constexpr int kKeys = 64;              // keys per slot
-constexpr int kAtom = kKeys * 128;     // bytes of a 64-column atom of 64 rows (tile or query)
-constexpr int kWorkers = 32 * (kSoftWarps + kWideWarps);
-constexpr int kMaxQ = (kHeads * 72 + kWorkers - 1) / kWorkers;  // 16-byte query pieces per worker at W = 576
 constexpr int kTasks = 4;              // widening tasks per warp and slot: 36 over 9 warps
 constexpr int kWeightLog2 = 6;         // weights enter the tensor cores scaled by 2^6
 constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceeded by 2^8
@@ -71,7 +59,7 @@ struct Mla4Params {
   float *part_o;   // [n_q, nsplit, H, R]      (nsplit > 1)
   float *part_ml;  // [n_q, nsplit, 2, H]
   int n_q, H, R, W, topk, nsplit;
-  uint32_t cpr_inv;  // ceil(2^20 / (W / 8)): t / (W / 8) = t * cpr_inv >> 20 for t < 64 * 72
+  uint32_t cpr_inv;  // query_pieces_inverse(W)
   float scale_log2;
   uint64_t wait_ns;
   int debug_stall;
@@ -108,158 +96,6 @@ __host__ __device__ inline Layout layout_of(int R, int W) {
 // tensor memory column of 128-column block mb of O^T
 __host__ __device__ inline int block_col(const Layout &l, int mb) {
   return 2 * kKeys + (mb < l.wide ? mb * kWideCols : l.wide * kWideCols + (mb - l.wide) * kHeads);
-}
-
-// barrier over `n` threads that also returns whether any of them passed true
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
-      : "memory");
-  return r != 0u;
-}
-__device__ __forceinline__ void bar_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-// whether the phase with the given parity has completed, without waiting:
-// mbarrier.try_wait may suspend the thread for a while, which would keep the
-// MMA warp from the other product it could issue
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
-// bounded wait that also gives up as soon as another role has failed
-__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
-                                             volatile uint32_t *failed) {
-  // the first tries do without the timer, whose reading takes hundreds of cycles
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*failed) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
-      *failed = 1u;
-      return false;
-    }
-  }
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major) {
-  return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-// D (+)= A . B^T, fp16 operands, issued by one lane of a converged warp
-__device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// one lane's commit: arrives once every MMA that lane issued has completed
-// (the same lane is elected each time)
-__device__ __forceinline__ void commit_elect(uint64_t *bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-// 16 lanes x 64 columns: thread t gets columns 8 i + 2 (t % 4) + {0, 1} of lane
-// t / 4 in r[4 i], r[4 i + 1] and of lane t / 4 + 8 in r[4 i + 2], r[4 i + 3]
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
-__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t x) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// loads of 16 and 8 bits into a 32-bit register as they are: a conversion after
-// the load would be waited for at once, and these are issued a slot ahead
-__device__ __forceinline__ uint32_t ldg_u16(const void *a) {
-  uint32_t v;
-  asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ldg_u8(const void *a) {
-  uint32_t v;
-  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(a));
-  return v;
-}
-__device__ __forceinline__ void prefetch_l2(const void *a) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
-}
-// w[t] = w[(t + n) % 4]
-__device__ __forceinline__ void rotate4(uint32_t (&w)[4], int n) {
-  const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
-  const bool one = n & 1, two = n & 2;
-  const uint32_t x0 = one ? b : a, x1 = one ? c : b, x2 = one ? d : c, x3 = one ? a : d;
-  w[0] = two ? x2 : x0;
-  w[1] = two ? x3 : x1;
-  w[2] = two ? x0 : x2;
-  w[3] = two ? x1 : x3;
-}
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
@@ -380,63 +216,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     return true;
   };
 
-  // The 64-head query tile (heads >= H zero), 128B-swizzled, K-major: every
-  // worker thread holds up to twelve 16-byte pieces in registers while the
-  // row's largest magnitude is found, then stores them scaled to fp16
-  float zscale = 0.f;  // logit units: log2(e) * scale / the query's power of two
-  if (worker) {
-    const int cpr = W / 8;  // 16-byte pieces per head
-    const int wtid = warp == kLastWideWarp ? kWorkers - 32 + lane : tid;
-    uint4 qv[kMaxQ];
-    if (nh > 0) {
-      const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(row) * p.H * W);
-#pragma unroll
-      for (int i = 0; i < kMaxQ; ++i) {
-        const int t = wtid + kWorkers * i;
-        qv[i] = t < p.H * cpr ? qrow[t] : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    float mx = 0.f;
-    if (nh > 0) {
-#pragma unroll
-      for (int i = 0; i < kMaxQ; ++i) {
-        const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
-                               fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) qmax[wtid >> 5] = mx;
-    bar_sync(2, kWorkers);
-#pragma unroll
-    for (int i = 0; i < kSoftWarps + kWideWarps; ++i) mx = fmaxf(mx, qmax[i]);
-    const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-    const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
-    const float f = pow2i(k);
-    zscale = p.scale_log2 * pow2i(-k);
-    if (nh > 0) {
-#pragma unroll
-      for (int i = 0; i < kMaxQ; ++i) {
-        const int t = wtid + kWorkers * i;
-        if (t < kHeads * cpr) {
-          const int h = static_cast<int>((static_cast<uint32_t>(t) * p.cpr_inv) >> 20);  // t / cpr
-          const int c = t - h * cpr;
-          const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            o[x] = pack_f16(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
-          sts_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(qready);
-  }
+  // logit units: log2(e) * scale / the query's power of two
+  float zscale = 0.f;
+  if (worker)
+    zscale = load_query_tile<true>(p.q + static_cast<int64_t>(row) * p.H * W, qs, p.H, W, p.cpr_inv,
+                                   nh > 0, warp == kLastWideWarp ? kWorkers - 32 + lane : tid, qmax,
+                                   qready) * p.scale_log2;
   if (warp < kSoftWarps) regs_inc<kSoftRegs>();
   else regs_dec<kOtherRegs>();
 
@@ -964,7 +749,7 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   p.W = W;
   p.topk = a.topk;
   p.nsplit = plan_splits(a.n_q, a.topk);
-  p.cpr_inv = ((1u << 20) + W / 8 - 1) / (W / 8);
+  p.cpr_inv = query_pieces_inverse(W);
   p.part_o = nullptr;
   p.part_ml = nullptr;
   if (p.nsplit > 1) {

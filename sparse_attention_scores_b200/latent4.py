@@ -39,14 +39,17 @@ class EvictStruct(ctypes.Structure):
                 ("dst_num_pages", ctypes.c_int32)]
 
 
-_ready = False
+_ready = _torch = None
+_CacheStruct, _byref = _dsa.CacheStruct, ctypes.byref
 
 
 def l4_lib() -> ctypes.CDLL:
     """The loaded library with the signatures of include/dsa_l4.h."""
-    global _ready
-    L = _dsa.lib()
-    if not _ready:
+    global _ready, _torch
+    if _ready is None:
+        import torch
+        _torch = torch
+        L = _dsa.lib()
         vp, sz, i32, i64, f32 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64,
                                  ctypes.c_float)
         pc, pd = ctypes.POINTER(_dsa.CacheStruct), ctypes.POINTER(_dsa.DimsStruct)
@@ -71,13 +74,19 @@ def l4_lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = res
-        _ready = True
-    return L
+        _ready = L
+    return _ready
+
+
+_lib_of = l4_lib
 
 
 def _types():
-    import torch
-    return torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.cuda.current_device()
+    """(bfloat16, float32, int32, uint8, the current device's index)"""
+    if _ready is None:
+        l4_lib()
+    t = _torch
+    return t.bfloat16, t.float32, t.int32, t.uint8, t.cuda.current_device()
 
 
 def _arg(t, name, dtype, device, shape=None, rows=False):
@@ -85,14 +94,14 @@ def _arg(t, name, dtype, device, shape=None, rows=False):
     rows: a 2-d tensor whose rows are contiguous, at any row stride."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, the call runs on cuda:{device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if not (t.is_contiguous() or (rows and t.dim() == 2 and t.stride(1) == 1 and
-                                  t.stride(0) >= t.shape[1])):
+    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1 and
+                                      t.stride(0) >= t.shape[1]):
         raise ValueError(f"{name}: not contiguous (strides {tuple(t.stride())})")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     return t.data_ptr()
 
@@ -104,12 +113,28 @@ def _pool(t, name, dtype, device, cache, width):
 
 def _common(cache, dims, ws, device, int32, uint8):
     """(cache struct, dims struct, workspace pointer, its size) of a call."""
-    _arg(cache.seq_lens, "seq_lens", int32, device)
-    _arg(cache.block_table, "block_table", int32, device)
-    if cache.block_table.dim() != 2 or cache.block_table.shape[0] != cache.seq_lens.shape[0]:
+    lens, table = cache.seq_lens, cache.block_table
+    lens_ptr, table_ptr = _arg(lens, "seq_lens", int32, device), _arg(table, "block_table", int32, device)
+    if table.dim() != 2 or lens.dim() != 1 or table.shape[0] != lens.shape[0]:
         raise ValueError("block_table: not [sequences, pages]")
-    return (ctypes.byref(cache.struct()), ctypes.byref(dims.struct()) if dims is not None else None,
-            _arg(ws, "ws", uint8, device), ws.numel())
+    seqs, pages = table.shape
+    return (_byref(_CacheStruct(seqs, lens_ptr, table_ptr, pages, cache.page_size, cache.num_pages,
+                                cache.max_seq_len)),
+            _byref(dims.struct()) if dims is not None else None, _arg(ws, "ws", uint8, device),
+            ws.numel())
+
+
+def _on(stream, device):
+    """The raw stream of a call: the given one, or the device's current one."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device) or None
+    return _dsa._stream(stream)
+
+
+def _row_bytes(dims, pool):
+    """The stored row's width; for an unsupported R or P the pool's own, so that
+    the library's refusal is the one that is raised."""
+    return _lib_of().dsa_l4_row_bytes(dims.R, dims.P) or pool.shape[2]
 
 
 def l4_row_bytes(R: int, P: int) -> int:
@@ -128,11 +153,10 @@ def l4_workspace_bytes(op: int, dims, cache) -> int:
 
 def l4_workspace(op: int, dims, cache, device="cuda", stream=None):
     """Allocate (with torch) and initialise a workspace for an L4_OP_* operation."""
-    import torch
     n = l4_workspace_bytes(op, dims, cache)
     if n == 0:
         raise _dsa.DsaError(1, "dsa_l4_workspace_bytes")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = _torch.empty(n, dtype=_torch.uint8, device=device)
     _dsa._check(_dsa.lib().dsa_workspace_init(ws.data_ptr(), n, _dsa._stream(stream)),
                 "dsa_workspace_init")
     return ws
@@ -146,13 +170,13 @@ def dsa_cache_append_l4(k_idx_new, latent_new, k_idx_pages, latent4_pages, cache
     bf16, _, i32, u8, dev = _types()
     L = l4_lib()
     c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = int(L.dsa_l4_row_bytes(dims.R, dims.P)) or latent4_pages.shape[2]
+    row = _row_bytes(dims, latent4_pages)
     _dsa._check(L.dsa_cache_append_l4(
         _arg(k_idx_new, "k_idx_new", bf16, dev, (dims.n_q, dims.D_I)),
         _arg(latent_new, "latent_new", bf16, dev, (dims.n_q, dims.R + dims.P)),
         _pool(k_idx_pages, "k_idx_pages", bf16, dev, cache, dims.D_I),
         _pool(latent4_pages, "latent4_pages", u8, dev, cache, row),
-        c, d, w, n, _dsa._stream(stream)), "dsa_cache_append_l4")
+        c, d, w, n, _on(stream, dev)), "dsa_cache_append_l4")
 
 
 def dsa_cache_read_l4(latent4_pages, cache, idx, dims, rows, ws, stream=None) -> None:
@@ -161,24 +185,24 @@ def dsa_cache_read_l4(latent4_pages, cache, idx, dims, rows, ws, stream=None) ->
     bf16, _, i32, u8, dev = _types()
     L = l4_lib()
     c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = int(L.dsa_l4_row_bytes(dims.R, dims.P)) or latent4_pages.shape[2]
+    row = _row_bytes(dims, latent4_pages)
     _dsa._check(L.dsa_cache_read_l4(
         _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c,
         _arg(idx, "idx", i32, dev, (dims.n_q, dims.topk)), d,
         _arg(rows, "rows", bf16, dev, (dims.n_q, dims.topk, dims.R + dims.P)),
-        w, n, _dsa._stream(stream)), "dsa_cache_read_l4")
+        w, n, _on(stream, dev)), "dsa_cache_read_l4")
 
 
 def _sparse_mla(fn, where, q, latent4_pages, cache, idx, dims, out, lse, ws, stream):
     bf16, f32, i32, u8, dev = _types()
     L = l4_lib()
     c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = int(L.dsa_l4_row_bytes(dims.R, dims.P)) or latent4_pages.shape[2]
+    row = _row_bytes(dims, latent4_pages)
     _dsa._check(fn(_arg(q, "q", bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)),
                    _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c,
                    _arg(idx, "idx", i32, dev, (dims.n_q, dims.topk)), d,
                    _arg(out, "out", f32, dev, (dims.n_q, dims.H, dims.R)),
-                   _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), w, n, _dsa._stream(stream)),
+                   _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), w, n, _on(stream, dev)),
                 where)
 
 
@@ -201,7 +225,7 @@ def dsa_attention_forward_l4(q_idx, w, k_idx_pages, q, latent4_pages, cache, dim
     bf16, f32, i32, u8, dev = _types()
     L = l4_lib()
     c, d, wsp, n = _common(cache, dims, ws, dev, i32, u8)
-    row = int(L.dsa_l4_row_bytes(dims.R, dims.P)) or latent4_pages.shape[2]
+    row = _row_bytes(dims, latent4_pages)
     _dsa._check(L.dsa_attention_forward_l4(
         _arg(q_idx, "q_idx", bf16, dev, (dims.n_q, dims.H_I, dims.D_I)),
         _arg(w, "w", f32, dev, (dims.n_q, dims.H_I)),
@@ -210,7 +234,7 @@ def dsa_attention_forward_l4(q_idx, w, k_idx_pages, q, latent4_pages, cache, dim
         _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c, d,
         _arg(idx_out, "idx_out", i32, dev, (dims.n_q, dims.topk)),
         _arg(out, "out", f32, dev, (dims.n_q, dims.H, dims.R)),
-        _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), wsp, n, _dsa._stream(stream)),
+        _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), wsp, n, _on(stream, dev)),
         "dsa_attention_forward_l4")
 
 
@@ -229,7 +253,7 @@ def _mass(fn, where, q, latent, cache, idx, lse, dims, decay, mass_in, mass_out,
                    _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), d, float(decay),
                    _arg(mass_in, "mass_in", f32, dev, rows=True),
                    _arg(mass_out, "mass_out", f32, dev, rows=True), ld, w, n,
-                   _dsa._stream(stream)), where)
+                   _on(stream, dev)), where)
 
 
 def dsa_attention_mass(q, latent_pages, cache, idx, lse, dims, decay, mass_in, mass_out, ws,
@@ -257,7 +281,7 @@ def dsa_attention_mass_l4(q, latent4_pages, cache, idx, lse, dims, decay, mass_i
                           stream=None) -> None:
     """dsa_attention_mass over a 4-bit latent cache."""
     t = _types()
-    row = int(l4_lib().dsa_l4_row_bytes(dims.R, dims.P)) or latent4_pages.shape[2]
+    row = _row_bytes(dims, latent4_pages)
     lat = (_pool(latent4_pages, "latent4_pages", t[3], t[4], cache, row),)
     _mass(l4_lib().dsa_attention_mass_l4, "dsa_attention_mass_l4", q, lat, cache, idx, lse, dims,
           decay, mass_in, mass_out, ws, stream, t)
@@ -314,5 +338,5 @@ def dsa_cache_evict(pools, cache, evict: Eviction, mass, dst_block_table, mass_d
         arr, len(pools), c, ctypes.byref(e), _arg(mass, "mass", f32, dev, rows=True), ld(mass),
         _arg(mass_dst, "mass_dst", f32, dev, rows=True), ld(mass_dst) if mass_dst is not None else 0,
         _arg(new_lens, "new_lens", i32, dev, (seqs,)),
-        _arg(kept, "kept", i32, dev, (seqs, evict.budget)), w, n, _dsa._stream(stream)),
+        _arg(kept, "kept", i32, dev, (seqs, evict.budget)), w, n, _on(stream, dev)),
         "dsa_cache_evict")

@@ -172,7 +172,10 @@ def test_binding_refuses_what_a_pointer_cannot_carry():
         latent4._arg(t, "t", torch.float32, 0)
 
     class Fake:  # a CUDA tensor's face
-        is_cuda, device, dtype = True, torch.device("cuda", 0), torch.float32
+        device, dtype = torch.device("cuda", 0), torch.float32
+
+        def get_device(self):
+            return 0
 
         def __init__(self, t):
             self.t = t
