@@ -6,7 +6,7 @@
 //            finite value (so that a protected token is never outranked)
 //   select   the exact top-k of the step (ties to the lower position,
 //            positions ascending)
-//   compact  one warp per kept token copies its row of every pool
+//   compact  a warp copies eight kept tokens' rows of every pool
 #include <float.h>
 #include <math.h>
 
@@ -57,12 +57,32 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const EvictParams p) {
   }
 }
 
+// kRows kept tokens per warp: a lane each resolves them, then the warp copies
+// their rows pool by pool, flattened over (row, unit), four units per lane in
+// flight.
+constexpr int kRows = 8;
 template <typename T>
-__device__ __forceinline__ void copy_row(const dsa_pool_t &q, int64_t src, int64_t dst, int lane) {
-  const int n = q.row_bytes / static_cast<int>(sizeof(T));
-  const T *s = static_cast<const T *>(q.src) + src * n;
-  T *d = static_cast<T *>(q.dst) + dst * n;
-  for (int i = lane; i < n; i += 32) d[i] = s[i];
+__device__ __forceinline__ void copy_rows(const dsa_pool_t &q, int src, int dst, int lane) {
+  const int n = q.row_bytes / static_cast<int>(sizeof(T));  // units per row
+  const uint32_t inv = ((1u << 20) + n - 1) / n;            // t / n = t * inv >> 20: t < 8 * 1,024
+  const T *s = static_cast<const T *>(q.src);
+  T *d = static_cast<T *>(q.dst);
+  for (int t0 = 0; t0 < kRows * n; t0 += 128) {
+    T v[4];
+    int64_t at[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + 32 * u + lane;
+      const int r = min(static_cast<int>((static_cast<uint64_t>(t) * inv) >> 20), kRows - 1);
+      const int c = t - r * n;
+      const int from = __shfl_sync(0xffffffffu, src, r), to = __shfl_sync(0xffffffffu, dst, r);
+      at[u] = t < kRows * n && from >= 0 ? static_cast<int64_t>(to) * n + c : -1;
+      if (at[u] >= 0) v[u] = s[static_cast<int64_t>(from) * n + c];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (at[u] >= 0) d[at[u]] = v[u];
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) {
@@ -70,20 +90,25 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) 
   griddep_launch_dependents();
   const int b = blockIdx.y, lane = lane_id();
   const int n = min(p.lens[b], p.budget);
-  for (int i = blockIdx.x * (kThreads / 32) + warp_id(); i < n; i += gridDim.x * (kThreads / 32)) {
-    const int pos = p.kept[b * p.kept_ld + i];
-    if (lane == 0 && p.mass_dst) p.mass_dst[b * p.mass_dst_ld + i] = p.mass[b * p.mass_ld + pos];
-    const int sp = p.src_table[static_cast<int64_t>(b) * p.src_max_pages + pos / kPageSize];
-    const int dp = p.dst_table[static_cast<int64_t>(b) * p.dst_max_pages + i / kPageSize];
-    if (sp < 0 || sp >= p.src_pages || dp < 0 || dp >= p.dst_pages) {
-      if (lane == 0) report(p.status, kErrBadPage, (kKernEvict << 24) | (i & 0xFFFF));
-      continue;
+  const int step = gridDim.x * (kThreads / 32) * kRows;
+  for (int i0 = (blockIdx.x * (kThreads / 32) + warp_id()) * kRows; i0 < n; i0 += step) {
+    const int i = i0 + lane;
+    int src = -1, dst = -1;
+    if (lane < kRows && i < n) {
+      const int pos = p.kept[b * p.kept_ld + i];
+      const int sp = p.src_table[static_cast<int64_t>(b) * p.src_max_pages + pos / kPageSize];
+      const int dp = p.dst_table[static_cast<int64_t>(b) * p.dst_max_pages + i / kPageSize];
+      if (p.mass_dst) p.mass_dst[b * p.mass_dst_ld + i] = p.mass[b * p.mass_ld + pos];
+      if (sp < 0 || sp >= p.src_pages || dp < 0 || dp >= p.dst_pages) {
+        report(p.status, kErrBadPage, (kKernEvict << 24) | (i & 0xFFFF));
+      } else {
+        src = sp * kPageSize + pos % kPageSize;
+        dst = dp * kPageSize + i % kPageSize;
+      }
     }
-    const int64_t src = static_cast<int64_t>(sp) * kPageSize + pos % kPageSize;
-    const int64_t dst = static_cast<int64_t>(dp) * kPageSize + i % kPageSize;
     for (int k = 0; k < p.n_pools; ++k) {
-      if (p.pools[k].row_bytes % 16 == 0) copy_row<uint4>(p.pools[k], src, dst, lane);
-      else copy_row<uint32_t>(p.pools[k], src, dst, lane);
+      if (p.pools[k].row_bytes % 16 == 0) copy_rows<uint4>(p.pools[k], src, dst, lane);
+      else copy_rows<uint32_t>(p.pools[k], src, dst, lane);
     }
   }
 }
@@ -133,8 +158,9 @@ dsa_status_t launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   const dsa_status_t st = launch_topk(t, stream);
   if (st != DSA_OK) return st;
   const int64_t most = std::min<int64_t>(a.evict.budget, a.cache.max_seq_len);
+  const int64_t per_cta = static_cast<int64_t>(kThreads / 32) * kRows;
   const unsigned rows = static_cast<unsigned>(
-      std::max<int64_t>(1, std::min<int64_t>(2048, (most + kThreads / 32 - 1) / (kThreads / 32))));
+      std::max<int64_t>(1, std::min<int64_t>(2048, (most + per_cta - 1) / per_cta)));
   return launch_pdl(compact_kernel, dim3(rows, B), dim3(kThreads), 0, stream, 1, p) == cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;

@@ -39,16 +39,17 @@ class EvictStruct(ctypes.Structure):
                 ("dst_num_pages", ctypes.c_int32)]
 
 
-_ready = _torch = None
-_CacheStruct, _byref = _dsa.CacheStruct, ctypes.byref
+_ready = _torch = _bf16 = _f32 = _i32 = _u8 = None
+_CacheStruct, _DimsStruct, _byref = _dsa.CacheStruct, _dsa.DimsStruct, ctypes.byref
 
 
 def l4_lib() -> ctypes.CDLL:
     """The loaded library with the signatures of include/dsa_l4.h."""
-    global _ready, _torch
+    global _ready, _torch, _bf16, _f32, _i32, _u8
     if _ready is None:
         import torch
         _torch = torch
+        _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
         L = _dsa.lib()
         vp, sz, i32, i64, f32 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64,
                                  ctypes.c_float)
@@ -78,15 +79,9 @@ def l4_lib() -> ctypes.CDLL:
     return _ready
 
 
-_lib_of = l4_lib
-
-
-def _types():
-    """(bfloat16, float32, int32, uint8, the current device's index)"""
-    if _ready is None:
-        l4_lib()
-    t = _torch
-    return t.bfloat16, t.float32, t.int32, t.uint8, t.cuda.current_device()
+def _device():
+    """The current CUDA device's index."""
+    return _torch.cuda.current_device() if not _torch.cuda.is_initialized() else _torch._C._cuda_getDevice()
 
 
 def _arg(t, name, dtype, device, shape=None, rows=False):
@@ -106,22 +101,19 @@ def _arg(t, name, dtype, device, shape=None, rows=False):
     return t.data_ptr()
 
 
-def _pool(t, name, dtype, device, cache, width):
-    """A page pool [num_pages, 64, width]."""
-    return _arg(t, name, dtype, device, (cache.num_pages, cache.page_size, width))
-
-
-def _common(cache, dims, ws, device, int32, uint8):
+def _common(cache, dims, ws, device):
     """(cache struct, dims struct, workspace pointer, its size) of a call."""
     lens, table = cache.seq_lens, cache.block_table
-    lens_ptr, table_ptr = _arg(lens, "seq_lens", int32, device), _arg(table, "block_table", int32, device)
-    if table.dim() != 2 or lens.dim() != 1 or table.shape[0] != lens.shape[0]:
+    lens_ptr, table_ptr = _arg(lens, "seq_lens", _i32, device), _arg(table, "block_table", _i32, device)
+    seqs, pages = table.shape if table.dim() == 2 else (-1, 0)
+    if lens.shape != (seqs,):
         raise ValueError("block_table: not [sequences, pages]")
-    seqs, pages = table.shape
     return (_byref(_CacheStruct(seqs, lens_ptr, table_ptr, pages, cache.page_size, cache.num_pages,
                                 cache.max_seq_len)),
-            _byref(dims.struct()) if dims is not None else None, _arg(ws, "ws", uint8, device),
-            ws.numel())
+            None if dims is None else
+            _byref(_DimsStruct(dims.n_q, dims.H_I, dims.D_I, dims.topk, dims.H, dims.R, dims.P,
+                               dims.causal, dims.q_pos0, dims.scale)),
+            _arg(ws, "ws", _u8, device), ws.numel())
 
 
 def _on(stream, device):
@@ -131,10 +123,14 @@ def _on(stream, device):
     return _dsa._stream(stream)
 
 
-def _row_bytes(dims, pool):
-    """The stored row's width; for an unsupported R or P the pool's own, so that
-    the library's refusal is the one that is raised."""
-    return _lib_of().dsa_l4_row_bytes(dims.R, dims.P) or pool.shape[2]
+def _pool4(t, device, cache, dims):
+    """A pool of 4-bit rows.  For an unsupported R or P any row width passes, so
+    that the library's refusal is the one that is raised."""
+    R, P = dims.R, dims.P
+    W = R + P
+    ok = 64 <= R <= 512 and R % 64 == 0 and P >= 0 and P % 16 == 0 and W <= 576
+    width = (W // 2 + W // 16 + 16) // 16 * 16 if ok else t.shape[-1]
+    return _arg(t, "latent4_pages", _u8, device, (cache.num_pages, cache.page_size, width))
 
 
 def l4_row_bytes(R: int, P: int) -> int:
@@ -167,93 +163,88 @@ def dsa_cache_append_l4(k_idx_new, latent_new, k_idx_pages, latent4_pages, cache
     """Write the new tokens' index keys [n_q, D_I] (bf16) and latent rows
     [n_q, R + P] (bf16, quantised to 4 bits) into the page pools at the
     positions of the step's query rows."""
-    bf16, _, i32, u8, dev = _types()
-    L = l4_lib()
-    c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = _row_bytes(dims, latent4_pages)
-    _dsa._check(L.dsa_cache_append_l4(
-        _arg(k_idx_new, "k_idx_new", bf16, dev, (dims.n_q, dims.D_I)),
-        _arg(latent_new, "latent_new", bf16, dev, (dims.n_q, dims.R + dims.P)),
-        _pool(k_idx_pages, "k_idx_pages", bf16, dev, cache, dims.D_I),
-        _pool(latent4_pages, "latent4_pages", u8, dev, cache, row),
-        c, d, w, n, _on(stream, dev)), "dsa_cache_append_l4")
+    L, dev = _ready or l4_lib(), _device()
+    c, d, w, n = _common(cache, dims, ws, dev)
+    status = L.dsa_cache_append_l4(
+        _arg(k_idx_new, "k_idx_new", _bf16, dev, (dims.n_q, dims.D_I)),
+        _arg(latent_new, "latent_new", _bf16, dev, (dims.n_q, dims.R + dims.P)),
+        _arg(k_idx_pages, "k_idx_pages", _bf16, dev, (cache.num_pages, cache.page_size, dims.D_I)),
+        _pool4(latent4_pages, dev, cache, dims), c, d, w, n, _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, "dsa_cache_append_l4")
 
 
 def dsa_cache_read_l4(latent4_pages, cache, idx, dims, rows, ws, stream=None) -> None:
     """The values of the stored rows at positions idx [n_q, topk], exactly, as
     bf16 rows [n_q, topk, R + P] (-1: a row of zeros)."""
-    bf16, _, i32, u8, dev = _types()
-    L = l4_lib()
-    c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = _row_bytes(dims, latent4_pages)
-    _dsa._check(L.dsa_cache_read_l4(
-        _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c,
-        _arg(idx, "idx", i32, dev, (dims.n_q, dims.topk)), d,
-        _arg(rows, "rows", bf16, dev, (dims.n_q, dims.topk, dims.R + dims.P)),
-        w, n, _on(stream, dev)), "dsa_cache_read_l4")
+    L, dev = _ready or l4_lib(), _device()
+    c, d, w, n = _common(cache, dims, ws, dev)
+    status = L.dsa_cache_read_l4(
+        _pool4(latent4_pages, dev, cache, dims), c, _arg(idx, "idx", _i32, dev, (dims.n_q, dims.topk)),
+        d, _arg(rows, "rows", _bf16, dev, (dims.n_q, dims.topk, dims.R + dims.P)), w, n,
+        _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, "dsa_cache_read_l4")
 
 
-def _sparse_mla(fn, where, q, latent4_pages, cache, idx, dims, out, lse, ws, stream):
-    bf16, f32, i32, u8, dev = _types()
-    L = l4_lib()
-    c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    row = _row_bytes(dims, latent4_pages)
-    _dsa._check(fn(_arg(q, "q", bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)),
-                   _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c,
-                   _arg(idx, "idx", i32, dev, (dims.n_q, dims.topk)), d,
-                   _arg(out, "out", f32, dev, (dims.n_q, dims.H, dims.R)),
-                   _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), w, n, _on(stream, dev)),
-                where)
+def _sparse_mla(where, q, latent4_pages, cache, idx, dims, out, lse, ws, stream):
+    L, dev = _ready or l4_lib(), _device()
+    c, d, w, n = _common(cache, dims, ws, dev)
+    nq, H = dims.n_q, dims.H
+    status = getattr(L, where)(
+        _arg(q, "q", _bf16, dev, (nq, H, dims.R + dims.P)), _pool4(latent4_pages, dev, cache, dims), c,
+        _arg(idx, "idx", _i32, dev, (nq, dims.topk)), d, _arg(out, "out", _f32, dev, (nq, H, dims.R)),
+        _arg(lse, "lse", _f32, dev, (nq, H)), w, n, _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, where)
 
 
 def dsa_sparse_mla_decode_l4(q, latent4_pages, cache, idx, dims, out, lse, ws, stream=None) -> None:
     """Sparse MLA decode over a 4-bit latent cache."""
-    _sparse_mla(l4_lib().dsa_sparse_mla_decode_l4, "dsa_sparse_mla_decode_l4", q, latent4_pages,
-                cache, idx, dims, out, lse, ws, stream)
+    _sparse_mla("dsa_sparse_mla_decode_l4", q, latent4_pages, cache, idx, dims, out, lse, ws, stream)
 
 
 def dsa_sparse_mla_prefill_l4(q, latent4_pages, cache, idx, dims, out, lse, ws,
                               stream=None) -> None:
     """Sparse MLA of causal prefill rows over a 4-bit latent cache."""
-    _sparse_mla(l4_lib().dsa_sparse_mla_prefill_l4, "dsa_sparse_mla_prefill_l4", q, latent4_pages,
-                cache, idx, dims, out, lse, ws, stream)
+    _sparse_mla("dsa_sparse_mla_prefill_l4", q, latent4_pages, cache, idx, dims, out, lse, ws, stream)
 
 
 def dsa_attention_forward_l4(q_idx, w, k_idx_pages, q, latent4_pages, cache, dims, idx_out, out,
                              lse, ws, stream=None) -> None:
     """The whole step over bf16 index keys and a 4-bit latent cache (idx_out may be None)."""
-    bf16, f32, i32, u8, dev = _types()
-    L = l4_lib()
-    c, d, wsp, n = _common(cache, dims, ws, dev, i32, u8)
-    row = _row_bytes(dims, latent4_pages)
-    _dsa._check(L.dsa_attention_forward_l4(
-        _arg(q_idx, "q_idx", bf16, dev, (dims.n_q, dims.H_I, dims.D_I)),
-        _arg(w, "w", f32, dev, (dims.n_q, dims.H_I)),
-        _pool(k_idx_pages, "k_idx_pages", bf16, dev, cache, dims.D_I),
-        _arg(q, "q", bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)),
-        _pool(latent4_pages, "latent4_pages", u8, dev, cache, row), c, d,
-        _arg(idx_out, "idx_out", i32, dev, (dims.n_q, dims.topk)),
-        _arg(out, "out", f32, dev, (dims.n_q, dims.H, dims.R)),
-        _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), wsp, n, _on(stream, dev)),
-        "dsa_attention_forward_l4")
+    L, dev = _ready or l4_lib(), _device()
+    c, d, wsp, n = _common(cache, dims, ws, dev)
+    nq, H = dims.n_q, dims.H
+    status = L.dsa_attention_forward_l4(
+        _arg(q_idx, "q_idx", _bf16, dev, (nq, dims.H_I, dims.D_I)),
+        _arg(w, "w", _f32, dev, (nq, dims.H_I)),
+        _arg(k_idx_pages, "k_idx_pages", _bf16, dev, (cache.num_pages, cache.page_size, dims.D_I)),
+        _arg(q, "q", _bf16, dev, (nq, H, dims.R + dims.P)), _pool4(latent4_pages, dev, cache, dims), c,
+        d, _arg(idx_out, "idx_out", _i32, dev, (nq, dims.topk)),
+        _arg(out, "out", _f32, dev, (nq, H, dims.R)), _arg(lse, "lse", _f32, dev, (nq, H)), wsp, n,
+        _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, "dsa_attention_forward_l4")
 
 
-def _mass(fn, where, q, latent, cache, idx, lse, dims, decay, mass_in, mass_out, ws, stream, types):
-    bf16, f32, i32, u8, dev = types
-    c, d, w, n = _common(cache, dims, ws, dev, i32, u8)
-    seqs = int(cache.seq_lens.shape[0])
-    ld = int(mass_out.stride(0)) if mass_out.dim() == 2 and seqs > 1 else int(mass_out.shape[-1])
+def _mass(where, q, latent, cache, idx, lse, dims, decay, mass_in, mass_out, ws, stream, dev):
+    c, d, w, n = _common(cache, dims, ws, dev)
+    seqs = cache.seq_lens.shape[0]
     if mass_out.dim() != 2 or mass_out.shape[0] != seqs:
         raise ValueError("mass_out: not [sequences, positions]")
+    ld = mass_out.stride(0) if seqs > 1 else mass_out.shape[1]
     if mass_in is not None and (mass_in.shape != mass_out.shape or
-                                (seqs > 1 and mass_in.stride(0) != mass_out.stride(0))):
+                                (seqs > 1 and mass_in.stride(0) != ld)):
         raise ValueError("mass_in: not laid out as mass_out")
-    _dsa._check(fn(_arg(q, "q", bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)), *latent, c,
-                   _arg(idx, "idx", i32, dev, (dims.n_q, dims.topk)),
-                   _arg(lse, "lse", f32, dev, (dims.n_q, dims.H)), d, float(decay),
-                   _arg(mass_in, "mass_in", f32, dev, rows=True),
-                   _arg(mass_out, "mass_out", f32, dev, rows=True), ld, w, n,
-                   _on(stream, dev)), where)
+    status = getattr(_ready, where)(
+        _arg(q, "q", _bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)), *latent, c,
+        _arg(idx, "idx", _i32, dev, (dims.n_q, dims.topk)),
+        _arg(lse, "lse", _f32, dev, (dims.n_q, dims.H)), d, float(decay),
+        _arg(mass_in, "mass_in", _f32, dev, rows=True),
+        _arg(mass_out, "mass_out", _f32, dev, rows=True), ld, w, n, _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, where)
 
 
 def dsa_attention_mass(q, latent_pages, cache, idx, lse, dims, decay, mass_in, mass_out, ws,
@@ -261,30 +252,31 @@ def dsa_attention_mass(q, latent_pages, cache, idx, lse, dims, decay, mass_in, m
     """Add the attention weight each kept token received to a running sum per
     token: mass_out = decay * mass_in + sum over heads of exp(z - lse), mass_*
     [sequences, positions] fp32 (mass_in None: zeros; mass_out may be mass_in)."""
-    t = _types()
-    lat = (_pool(latent_pages, "latent_pages", t[0], t[4], cache, dims.R + dims.P),)
-    _mass(l4_lib().dsa_attention_mass, "dsa_attention_mass", q, lat, cache, idx, lse, dims, decay,
-          mass_in, mass_out, ws, stream, t)
+    _ready or l4_lib()
+    dev = _device()
+    lat = (_arg(latent_pages, "latent_pages", _bf16, dev,
+                (cache.num_pages, cache.page_size, dims.R + dims.P)),)
+    _mass("dsa_attention_mass", q, lat, cache, idx, lse, dims, decay, mass_in, mass_out, ws, stream, dev)
 
 
 def dsa_attention_mass_l8(q, latent8_pages, latent_scale, cache, idx, lse, dims, decay, mass_in,
                           mass_out, ws, stream=None) -> None:
     """dsa_attention_mass over E4M3 latent rows with one fp32 scale per token."""
-    t = _types()
-    lat = (_pool(latent8_pages, "latent8_pages", t[3], t[4], cache, dims.R + dims.P),
-           _arg(latent_scale, "latent_scale", t[1], t[4], (cache.num_pages * cache.page_size,)))
-    _mass(l4_lib().dsa_attention_mass_l8, "dsa_attention_mass_l8", q, lat, cache, idx, lse, dims,
-          decay, mass_in, mass_out, ws, stream, t)
+    _ready or l4_lib()
+    dev = _device()
+    lat = (_arg(latent8_pages, "latent8_pages", _u8, dev,
+                (cache.num_pages, cache.page_size, dims.R + dims.P)),
+           _arg(latent_scale, "latent_scale", _f32, dev, (cache.num_pages * cache.page_size,)))
+    _mass("dsa_attention_mass_l8", q, lat, cache, idx, lse, dims, decay, mass_in, mass_out, ws, stream, dev)
 
 
 def dsa_attention_mass_l4(q, latent4_pages, cache, idx, lse, dims, decay, mass_in, mass_out, ws,
                           stream=None) -> None:
     """dsa_attention_mass over a 4-bit latent cache."""
-    t = _types()
-    row = _row_bytes(dims, latent4_pages)
-    lat = (_pool(latent4_pages, "latent4_pages", t[3], t[4], cache, row),)
-    _mass(l4_lib().dsa_attention_mass_l4, "dsa_attention_mass_l4", q, lat, cache, idx, lse, dims,
-          decay, mass_in, mass_out, ws, stream, t)
+    _ready or l4_lib()
+    dev = _device()
+    _mass("dsa_attention_mass_l4", q, (_pool4(latent4_pages, dev, cache, dims),), cache, idx, lse,
+          dims, decay, mass_in, mass_out, ws, stream, dev)
 
 
 @dataclass
@@ -306,37 +298,37 @@ def dsa_cache_evict(pools, cache, evict: Eviction, mass, dst_block_table, mass_d
     [sequences, positions] fp32 or None; new_lens [sequences] int32; kept
     [sequences, budget] int32 or None.
     """
-    _, f32, i32, u8, dev = _types()
-    L = l4_lib()
-    c, _, w, n = _common(cache, None, ws, dev, i32, u8)
-    seqs = int(cache.seq_lens.shape[0])
+    L, dev = _ready or l4_lib(), _device()
+    c, _, w, n = _common(cache, None, ws, dev)
+    seqs, size = cache.seq_lens.shape[0], cache.page_size
     if len(pools) > EVICT_MAX_POOLS:
         raise ValueError(f"pools: {len(pools)}, at most {EVICT_MAX_POOLS}")
     arr = (PoolStruct * max(1, len(pools)))()
     dst_pages = None
     for i, (src, dst) in enumerate(pools):
-        if src.dtype is not dst.dtype or src.shape[1:] != dst.shape[1:] or \
-                src.shape[0] != cache.num_pages or src.dim() < 2 or src.shape[1] != cache.page_size:
-            raise ValueError(f"pools[{i}]: source {tuple(src.shape)} {src.dtype}, "
-                             f"destination {tuple(dst.shape)} {dst.dtype}")
-        if dst_pages not in (None, int(dst.shape[0])):
+        sh, dh = src.shape, dst.shape
+        if src.dtype is not dst.dtype or sh[1:] != dh[1:] or len(sh) < 2 or sh[0] != cache.num_pages \
+                or sh[1] != size:
+            raise ValueError(f"pools[{i}]: source {tuple(sh)} {src.dtype}, destination {tuple(dh)} {dst.dtype}")
+        if dst_pages is not None and dst_pages != dh[0]:
             raise ValueError(f"pools[{i}]: destination pools of different sizes")
-        dst_pages = int(dst.shape[0])
-        arr[i].src = _arg(src, f"pools[{i}] source", src.dtype, dev)
-        arr[i].dst = _arg(dst, f"pools[{i}] destination", dst.dtype, dev)
-        arr[i].row_bytes = src.element_size() * (src.numel() // (src.shape[0] * src.shape[1]))
+        dst_pages = dh[0]
+        arr[i] = (_arg(src, "pool source", src.dtype, dev), _arg(dst, "pool destination", dst.dtype, dev),
+                  src.element_size() * (src.numel() // (sh[0] * size)))
     if dst_block_table.dim() != 2 or dst_block_table.shape[0] != seqs:
         raise ValueError("dst_block_table: not [sequences, pages]")
     for name, t in (("mass", mass), ("mass_dst", mass_dst)):
         if t is not None and (t.dim() != 2 or t.shape[0] != seqs):
             raise ValueError(f"{name}: not [sequences, positions]")
-    ld = lambda t: int(t.stride(0)) if seqs > 1 else int(t.shape[1])  # noqa: E731
+    wide = 0 if seqs > 1 else 1  # row stride, or the width of a single row
     e = EvictStruct(evict.budget, evict.sinks, evict.recent,
-                    _arg(dst_block_table, "dst_block_table", i32, dev),
-                    int(dst_block_table.shape[1]), dst_pages if dst_pages is not None else 1 << 24)
-    _dsa._check(L.dsa_cache_evict(
-        arr, len(pools), c, ctypes.byref(e), _arg(mass, "mass", f32, dev, rows=True), ld(mass),
-        _arg(mass_dst, "mass_dst", f32, dev, rows=True), ld(mass_dst) if mass_dst is not None else 0,
-        _arg(new_lens, "new_lens", i32, dev, (seqs,)),
-        _arg(kept, "kept", i32, dev, (seqs, evict.budget)), w, n, _on(stream, dev)),
-        "dsa_cache_evict")
+                    _arg(dst_block_table, "dst_block_table", _i32, dev), dst_block_table.shape[1],
+                    dst_pages if dst_pages is not None else 1 << 24)
+    status = L.dsa_cache_evict(
+        arr, len(pools), c, _byref(e), _arg(mass, "mass", _f32, dev, rows=True),
+        mass.shape[1] if wide else mass.stride(0), _arg(mass_dst, "mass_dst", _f32, dev, rows=True),
+        0 if mass_dst is None else mass_dst.shape[1] if wide else mass_dst.stride(0),
+        _arg(new_lens, "new_lens", _i32, dev, (seqs,)), _arg(kept, "kept", _i32, dev, (seqs, evict.budget)),
+        w, n, _on(stream, dev))
+    if status:
+        raise _dsa.DsaError(status, "dsa_cache_evict")
