@@ -78,7 +78,8 @@ size_t ws_bytes_for(dsa_l4_op_t op, const dsa_dims_t &d, const dsa_cache_t &c) {
 
 dsa_status_t run_mla4(const uint16_t *q, const uint8_t *latent, const dsa_cache_t &c,
                       const int32_t *idx, const dsa_dims_t &d, float *out, float *lse,
-                      void *scratch, size_t scratch_bytes, DevStatus *st, cudaStream_t s) {
+                      void *scratch, size_t scratch_bytes, DevStatus *st, cudaStream_t s,
+                      int early_q = 0) {
   Mla4Launch a;
   a.q = q;
   a.latent = latent;
@@ -95,6 +96,7 @@ dsa_status_t run_mla4(const uint16_t *q, const uint8_t *latent, const dsa_cache_
   a.scratch = scratch;
   a.scratch_bytes = scratch_bytes;
   a.status = st;
+  a.early_q = early_q;
   return launch_mla4(a, s);
 }
 
@@ -281,7 +283,7 @@ dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float *w,
                    ws_bytes, stream));
   return run_mla4(q, latent4_pages, c, idx, d, out, lse, at,
                   ws_bytes - static_cast<size_t>(at - static_cast<uint8_t *>(ws)), status_of(ws),
-                  as_stream(stream));
+                  as_stream(stream), /*early_q=*/1);
 }
 
 dsa_status_t dsa_attention_mass(const uint16_t *q, const uint16_t *latent_pages,

@@ -54,6 +54,9 @@ struct Mla4Launch {
   void *scratch;
   size_t scratch_bytes;
   DevStatus *status;
+  // 1: q is complete before the kernel preceding this one in the stream started
+  // (the whole step), so its tile is written before that kernel has ended
+  int early_q = 0;
 };
 size_t mla4_scratch_bytes(int n_q, int topk, int R);
 dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream);

@@ -180,56 +180,57 @@ __host__ inline uint32_t query_pieces_inverse(int W) { return ((1u << 20) + W / 
 
 // The 64-head query tile of one row (heads >= H zero), 128B-swizzled, K-major,
 // by the worker threads (wtid in [0, kWorkers)), each holding up to twelve
-// 16-byte pieces.  kScaled: as fp16, scaled by the power of two that puts the
-// row's largest magnitude in [2^14, 2^15) (one pass: the pieces stay in
-// registers while the largest is found); returns that power's inverse.  Else
-// as it is (bf16), and 1.  Each worker warp arrives on qready once.
-template <bool kScaled>
-__device__ __forceinline__ float load_query_tile(const uint16_t *q, uint32_t qs, int H, int W,
-                                                 uint32_t cpr_inv, bool any, int wtid, float *qmax,
-                                                 uint64_t *qready) {
-  const int cpr = W / 8, lane = lane_id();  // 16-byte pieces per head
-  const uint4 *src = reinterpret_cast<const uint4 *>(q);
-  uint4 qv[kMaxQ];
-  if (any) {
+// 16-byte pieces: load() issues the loads, store() writes the tile.  One pass over
+// the row: the pieces stay in registers while its largest magnitude is found.
+struct QueryPieces {
+  uint4 v[kMaxQ];
+
+  __device__ __forceinline__ void load(const uint16_t *q, int H, int W, int wtid) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(q);
+    const int n = H * (W / 8);
 #pragma unroll
     for (int i = 0; i < kMaxQ; ++i) {
       const int t = wtid + kWorkers * i;
-      qv[i] = t < H * cpr ? src[t] : make_uint4(0u, 0u, 0u, 0u);
+      v[i] = t < n ? src[t] : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  float f = 1.f, inv = 1.f;
-  if constexpr (kScaled) {
+
+  // the exponent of the power of two that puts the row's largest magnitude in
+  // [2^14, 2^15) (all workers call it: they meet at a barrier)
+  __device__ __forceinline__ int scale_exponent(int wtid, float *qmax) const {
     float mx = 0.f;
-    if (any) {
 #pragma unroll
-      for (int i = 0; i < kMaxQ; ++i) {
-        const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+    for (int i = 0; i < kMaxQ; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
-                               fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
-      }
+      for (int t = 0; t < 4; ++t)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[t] << 16)),
+                             fabsf(__uint_as_float(w[t] & 0xFFFF0000u))));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) qmax[wtid >> 5] = mx;
+    if (lane_id() == 0) qmax[wtid >> 5] = mx;
     bar_sync(2, kWorkers);
 #pragma unroll
     for (int i = 0; i < kSoftWarps + kWideWarps; ++i) mx = fmaxf(mx, qmax[i]);
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-    const int k = mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
-    f = pow2i(k);
-    inv = pow2i(-k);
+    return mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
   }
-  if (any) {
+
+  // kScaled: as fp16, times 2^k; else as it is (bf16).  Each worker warp
+  // arrives on qready once.
+  template <bool kScaled>
+  __device__ __forceinline__ void store(uint32_t qs, int W, uint32_t cpr_inv, int wtid, int k,
+                                        uint64_t *qready) const {
+    const int cpr = W / 8;  // 16-byte pieces per head
+    const float f = pow2i(k);
 #pragma unroll
     for (int i = 0; i < kMaxQ; ++i) {
       const int t = wtid + kWorkers * i;
       if (t < kHeads * cpr) {
         const int h = static_cast<int>((static_cast<uint32_t>(t) * cpr_inv) >> 20);  // t / cpr
         const int c = t - h * cpr;
-        uint32_t o[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        uint32_t o[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         if constexpr (kScaled) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -238,11 +239,10 @@ __device__ __forceinline__ float load_query_tile(const uint16_t *q, uint32_t qs,
         sts_v4(qs + (c >> 3) * kAtom + h * 128 + (((c & 7) ^ (h & 7)) << 4), o[0], o[1], o[2], o[3]);
       }
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(qready);
   }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(qready);
-  return inv;
-}
+};
 
 }  // namespace dsa

@@ -160,11 +160,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
 
   const bool worker = warp < kMmaWarp || warp == kLastWideWarp;
   float zscale = 0.f;
-  if (worker)
-    zscale = load_query_tile<F != kLatBf16>(p.q + static_cast<int64_t>(row) * p.H * W, qs, p.H, W,
-                                            p.cpr_inv, nh > 0,
-                                            warp == kLastWideWarp ? kWorkers - 32 + lane : tid, qmax,
-                                            qready) * p.scale_log2;
+  if (worker && nh > 0) {
+    const int wtid = warp == kLastWideWarp ? kWorkers - 32 + lane : tid;
+    QueryPieces q;
+    q.load(p.q + static_cast<int64_t>(row) * p.H * W, p.H, W, wtid);
+    const int k = F != kLatBf16 ? q.scale_exponent(wtid, qmax) : 0;
+    zscale = pow2i(-k) * p.scale_log2;
+    q.store<F != kLatBf16>(qs, W, p.cpr_inv, wtid, k, qready);
+  }
   if (warp < kSoftWarps) regs_inc<kSoftRegs>();
   else regs_dec<kOtherRegs>();
 

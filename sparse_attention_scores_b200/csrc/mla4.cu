@@ -21,7 +21,7 @@
 //   warps 0-3    softmax of each slot (warp w: heads 16 w ..),
 //                the rare rescale of O
 //   (both kinds load the query tile first)
-//   warps 4-11, 14   widening: decode a slot from registers, into which the next
+//   warps 4-11, 14  widening: decode a slot from registers, into which the next
 //                slot's bytes are loaded as soon as they are free
 //   warp 13      turns the selected positions into pool rows, ahead of them
 //   warp 12      issues the MMAs: S of a slot as soon as it is
@@ -59,9 +59,11 @@ struct Mla4Params {
   float *part_o;   // [n_q, nsplit, H, R]      (nsplit > 1)
   float *part_ml;  // [n_q, nsplit, 2, H]
   int n_q, H, R, W, topk, nsplit;
+  int ncb;  // CTAs that share a split's output columns
   uint32_t cpr_inv;  // query_pieces_inverse(W)
   float scale_log2;
   uint64_t wait_ns;
+  int early_q;  // q is complete before the kernel before this one started
   int debug_stall;
   DevStatus *status;
 };
@@ -74,18 +76,13 @@ struct Mla4Params {
 // lo | hi): a wide block of O^T takes both terms in one instruction, at 64
 // cycles against 2 x 48 (measured), and keeps their sums apart until the end.
 struct Layout {
-  int nQ, nmb;        // query atoms, 128-column blocks of O^T
-  int wide;           // blocks whose two terms accumulate side by side
+  int nQ, nmb;        // query atoms, 128-column blocks of the latent rows
   uint32_t off_p, off_tile1, off_q, off_misc, bytes;
 };
-constexpr int kWideCols = 128;  // tensor memory columns of a wide block, against 64
 __host__ __device__ inline Layout layout_of(int R, int W) {
   Layout l;
   l.nQ = (W + 63) / 64;
   l.nmb = (R + 127) / 128;
-  // 512 columns: two S buffers of 64, then the blocks
-  const int spare = (512 - 2 * kKeys) / kHeads - l.nmb;
-  l.wide = l.nmb < spare ? l.nmb : spare;
   l.off_p = 2u * l.nmb * kAtom;
   l.off_tile1 = l.off_p + 3u * kAtom;
   l.off_q = l.off_tile1 + 2u * l.nmb * kAtom;
@@ -93,10 +90,19 @@ __host__ __device__ inline Layout layout_of(int R, int W) {
   l.bytes = l.off_misc + kMisc;
   return l;
 }
-// tensor memory column of 128-column block mb of O^T
-__host__ __device__ inline int block_col(const Layout &l, int mb) {
-  return 2 * kKeys + (mb < l.wide ? mb * kWideCols : l.wide * kWideCols + (mb - l.wide) * kHeads);
-}
+// Tensor memory: S of slot s at columns 64 s, then the CTA's n blocks of O^T,
+// `wide` of which keep the sums of the two terms side by side.
+constexpr int kWideCols = 128;  // columns of a wide block, against 64
+struct Blocks {
+  int n, wide;
+  __device__ __forceinline__ explicit Blocks(int blocks) : n(blocks) {
+    const int spare = (512 - 2 * kKeys) / kHeads - blocks;
+    wide = blocks < spare ? blocks : spare;
+  }
+  __device__ __forceinline__ int col(int mb) const {
+    return 2 * kKeys + (mb < wide ? mb * kWideCols : wide * kWideCols + (mb - wide) * kHeads);
+  }
+};
 
 __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -128,12 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   float *lfin = mfin + kHeads;
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
-  const int split = blockIdx.x;
+  const int split = blockIdx.x;  // blockIdx.z: the output columns
   // causal rows grow with their number: the longest ones start first
   const int row = p.rows.causal ? p.n_q - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
 
   // tensor memory: S of slot s at columns 64 s, O^T from column 128
-  const int o_cols = block_col(lay, lay.nmb) - 2 * kKeys;
+  const Blocks ob(lay.nmb / p.ncb);  // this CTA's blocks of O^T, from mb0
+  const int mb0 = static_cast<int>(blockIdx.z) * ob.n;
+  const int o_cols = ob.col(ob.n) - 2 * kKeys;
   uint32_t tmem_cols = 32;
   while (tmem_cols < static_cast<uint32_t>(2 * kKeys + o_cols)) tmem_cols <<= 1;
   if (tid == 0) {
@@ -155,6 +163,22 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   if (warp == kMmaWarp) {
     tmem_alloc(const_cast<uint32_t *>(&misc[0]), tmem_cols);
     tmem_relinquish();
+  }
+  const bool worker = warp < kMmaWarp || warp == kLastWideWarp;
+  const int wtid = warp == kLastWideWarp ? kWorkers - 32 + lane : tid;
+  const uint16_t *qrow = p.q + static_cast<int64_t>(row) * p.H * W;
+  float zscale = 0.f;  // logit units: log2(e) * scale / the query's power of two
+  // in the whole step q predates the kernel before this one: its tile is
+  // written under that kernel's tail
+  if (p.early_q) {
+    __syncthreads();
+    if (worker) {
+      QueryPieces q;
+      q.load(qrow, p.H, W, wtid);
+      const int k = q.scale_exponent(wtid, qmax);
+      zscale = pow2i(-k) * p.scale_log2;
+      q.store<true>(qs, W, p.cpr_inv, wtid, k, qready);
+    }
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -182,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   // sixteen lanes side by side per row (with four lanes per row the loads took
   // twice the cache lines each, and the load path, which the tile's stores
   // share, was the limit); task 32 + t: units 16 and 17 of rows 16 t .. 16 t + 15.
-  const bool worker = warp < kMmaWarp || warp == kLastWideWarp;
   const int g = warp == kLastWideWarp ? kWideWarps - 1 : warp - kSoftWarps, nb = W / kL4Block, units = (nb + 1) / 2, rb = l4_row_bytes(W);
   auto task_row = [&](int i) {
     const int t = g + kWideWarps * i;
@@ -216,12 +239,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     return true;
   };
 
-  // logit units: log2(e) * scale / the query's power of two
-  float zscale = 0.f;
-  if (worker)
-    zscale = load_query_tile<true>(p.q + static_cast<int64_t>(row) * p.H * W, qs, p.H, W, p.cpr_inv,
-                                   nh > 0, warp == kLastWideWarp ? kWorkers - 32 + lane : tid, qmax,
-                                   qready) * p.scale_log2;
+  bool loaded = false;
+  if (worker && !p.early_q && nh > 0) {
+    QueryPieces q;
+    q.load(qrow, p.H, W, wtid);
+    const int k = q.scale_exponent(wtid, qmax);
+    zscale = pow2i(-k) * p.scale_log2;
+    q.store<true>(qs, W, p.cpr_inv, wtid, k, qready);
+    if (warp >= kSoftWarps) loaded = load_rows(0);
+  } else if (worker && warp >= kSoftWarps && nh > 0) {
+    loaded = load_rows(0);
+  }
   if (warp < kSoftWarps) regs_inc<kSoftRegs>();
   else regs_dec<kOtherRegs>();
 
@@ -354,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     }
   } else if (worker) {
     // -------------------------------------------------------------- widening
-    bool loaded = nh > 0 && load_rows(0);
     for (int j = 0; j < nh && loaded; ++j) {
       const int s = j & 1;
       if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
@@ -487,15 +514,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         tc_fence_after();
         const int s = npv & 1;
         const uint32_t more = npv > 0 ? 1u : 0u;
-        const uint64_t d_v = smem_desc(tile_u + s * lay.off_tile1, kAtom, 1024, kLayoutSW128);
+        const uint64_t d_v = smem_desc(tile_u + s * lay.off_tile1 + 2 * mb0 * kAtom, kAtom, 1024, kLayoutSW128);
         const uint64_t d_both = smem_desc(p_u + s * kAtom, 16, 1024, kLayoutSW128);
         const uint64_t d_hi = smem_desc(p_u + 2 * s * kAtom, 16, 1024, kLayoutSW128);
         const uint64_t d_lo = smem_desc(p_u + kAtom, 16, 1024, kLayoutSW128);
-        const uint32_t o = tm + 2 * kKeys, on = o + lay.wide * kWideCols;  // wide, narrow blocks
-        const uint64_t d_vn = d_v + ((lay.wide * 2 * kAtom) >> 4);
-        const int narrow = lay.nmb - lay.wide;
+        const uint32_t o = tm + 2 * kKeys, on = o + ob.wide * kWideCols;  // wide, narrow blocks
+        const uint64_t d_vn = d_v + ((ob.wide * 2 * kAtom) >> 4);
+        const int narrow = ob.n - ob.wide;
 #pragma unroll 2
-        for (int mb = 0; mb < lay.wide; ++mb)
+        for (int mb = 0; mb < ob.wide; ++mb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f16_elect(o + mb * kWideCols, d_v + ((2 * mb * kAtom + k * 2048) >> 4),
@@ -559,14 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   }
   if (warp < kOutWarps && (have_o || p.nsplit == 1)) {
     const int q4 = warp & 3;
-    for (int u = warp >> 2; u < 2 * lay.nmb; u += kOutWarps / 4) {
+    for (int u = warp >> 2; u < 2 * ob.n; u += kOutWarps / 4) {
       const int mb = u >> 1, hb = 32 * (u & 1);
       if (hb >= p.H) continue;
       uint32_t v[32];
       if (have_o) {
-        const uint32_t ta = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + block_col(lay, mb) + hb;
+        const uint32_t ta = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + ob.col(mb) + hb;
         tmem_ld_32x32b_x32(ta, v);
-        if (mb < lay.wide) {
+        if (mb < ob.wide) {
           uint32_t w[32];
           tmem_ld_32x32b_x32(ta + kHeads, w);
           tmem_ld_wait();
@@ -577,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
           tmem_ld_wait();
         }
       }
-      const int c = mb * 128 + q4 * 32 + lane, left = p.H - hb;
+      const int c = (mb0 + mb) * 128 + q4 * 32 + lane, left = p.H - hb;
       if (c < R) {
         float *at = dst + static_cast<int64_t>(hb) * R + c;
 #pragma unroll
@@ -590,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       }
     }
   }
-  if (tid < p.H) {
+  if (tid < p.H && mb0 == 0) {
     if (p.nsplit == 1) {
       const float l = lfin[tid];
       p.lse[static_cast<int64_t>(row) * p.H + tid] =
@@ -761,9 +788,19 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   }
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.wait_ns = wait_limit_ns();
+  p.early_q = a.early_q;
   p.debug_stall = debug_stall() == static_cast<int>(kKernMla4) ? 1 : 0;
   p.status = a.status;
-  if (launch_pdl(mla4_kernel, dim3(static_cast<unsigned>(p.nsplit), static_cast<unsigned>(a.n_q)),
+  // While CTAs still leave SMs idle, a split's output columns go to 2 or 4 of
+  // them: each forms the logits anew, but multiplies and stores its share only
+  // (one row of top-2,048: 15.8 us with one CTA a split, 13.3 with four).
+  const int nmb = (a.R + 127) / 128;
+  p.ncb = 1;
+  for (int c = 2; c <= 4; c *= 2)
+    if (nmb % c == 0 && static_cast<int64_t>(a.n_q) * p.nsplit * c <= device_sm_count()) p.ncb = c;
+  if (launch_pdl(mla4_kernel,
+                 dim3(static_cast<unsigned>(p.nsplit), static_cast<unsigned>(a.n_q),
+                      static_cast<unsigned>(p.ncb)),
                  dim3(kThreads), smem, stream, 1u, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   if (p.nsplit == 1) return DSA_OK;
