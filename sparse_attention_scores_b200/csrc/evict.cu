@@ -6,7 +6,7 @@
 //            finite value (so that a protected token is never outranked)
 //   select   the exact top-k of the step (ties to the lower position,
 //            positions ascending)
-//   compact  a warp copies eight kept tokens' rows of every pool
+//   compact  a warp copies a few kept tokens' rows of every pool
 #include <float.h>
 #include <math.h>
 
@@ -58,20 +58,23 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const EvictParams p) {
 }
 
 // kRows kept tokens per warp: a lane each resolves them, then the warp copies
-// their rows pool by pool, flattened over (row, unit), four units per lane in
-// flight.
-constexpr int kRows = 8;
-template <typename T>
+// their rows pool by pool, flattened over (row, unit), kFlight units per lane in
+// flight: four rows of 336 bytes are 84 units, of 256 bytes 64.  Four rows where
+// they fill the device, two where they do not (latency).  4 x 131,072 tokens to
+// 16,384, 592 bytes each, the whole call: 36.6 us; eight rows and four or six
+// units in flight 38.9 and 39.5, two rows 41.0.
+constexpr int kFlight = 3;
+template <int kRows, typename T>
 __device__ __forceinline__ void copy_rows(const dsa_pool_t &q, int src, int dst, int lane) {
   const int n = q.row_bytes / static_cast<int>(sizeof(T));  // units per row
-  const uint32_t inv = ((1u << 20) + n - 1) / n;            // t / n = t * inv >> 20: t < 8 * 1,024
+  const uint32_t inv = ((1u << 20) + n - 1) / n;            // t / n = t * inv >> 20: t < 4 * 1,024
   const T *s = static_cast<const T *>(q.src);
   T *d = static_cast<T *>(q.dst);
-  for (int t0 = 0; t0 < kRows * n; t0 += 128) {
-    T v[4];
-    int64_t at[4];
+  for (int t0 = 0; t0 < kRows * n; t0 += 32 * kFlight) {
+    T v[kFlight];
+    int64_t at[kFlight];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kFlight; ++u) {
       const int t = t0 + 32 * u + lane;
       const int r = min(static_cast<int>((static_cast<uint64_t>(t) * inv) >> 20), kRows - 1);
       const int c = t - r * n;
@@ -80,11 +83,12 @@ __device__ __forceinline__ void copy_rows(const dsa_pool_t &q, int src, int dst,
       if (at[u] >= 0) v[u] = s[static_cast<int64_t>(from) * n + c];
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kFlight; ++u)
       if (at[u] >= 0) d[at[u]] = v[u];
   }
 }
 
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -107,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) 
       }
     }
     for (int k = 0; k < p.n_pools; ++k) {
-      if (p.pools[k].row_bytes % 16 == 0) copy_rows<uint4>(p.pools[k], src, dst, lane);
-      else copy_rows<uint32_t>(p.pools[k], src, dst, lane);
+      if (p.pools[k].row_bytes % 16 == 0) copy_rows<kRows, uint4>(p.pools[k], src, dst, lane);
+      else copy_rows<kRows, uint32_t>(p.pools[k], src, dst, lane);
     }
   }
 }
@@ -158,10 +162,11 @@ dsa_status_t launch_evict(const EvictLaunch &a, cudaStream_t stream) {
   const dsa_status_t st = launch_topk(t, stream);
   if (st != DSA_OK) return st;
   const int64_t most = std::min<int64_t>(a.evict.budget, a.cache.max_seq_len);
-  const int64_t per_cta = static_cast<int64_t>(kThreads / 32) * kRows;
+  const bool many = most * B >= static_cast<int64_t>(device_sm_count()) * 128;
+  const int64_t per_cta = static_cast<int64_t>(kThreads / 32) * (many ? 4 : 2);
   const unsigned rows = static_cast<unsigned>(
       std::max<int64_t>(1, std::min<int64_t>(2048, (most + per_cta - 1) / per_cta)));
-  return launch_pdl(compact_kernel, dim3(rows, B), dim3(kThreads), 0, stream, 1, p) == cudaSuccess
+  return launch_pdl(many ? compact_kernel<4> : compact_kernel<2>, dim3(rows, B), dim3(kThreads), 0, stream, 1, p) == cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;
 }

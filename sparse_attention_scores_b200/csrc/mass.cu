@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     tmem_alloc(const_cast<uint32_t *>(&misc[0]), 2 * kKeys);
     tmem_relinquish();
   }
-  griddep_wait();
+  // What this kernel reads is older than decay_kernel, which had waited for it
+  // before it let this one start; only the sums have to wait for decay_kernel
+  // itself (before their first add).
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       return j < nh && at < nsel ? idx[at] : -1;
     };
     int pos[2] = {place(0, 0), place(0, 1)};
+    griddep_wait();
     for (int j = 0; j < nh; ++j) {
       const int s = j & 1;
       const uint32_t par = (j >> 1) & 1;
