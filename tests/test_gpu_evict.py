@@ -239,6 +239,58 @@ def test_evict_reports_pages_out_of_range():
     assert st[0] == 6 and st[1] >> 24 == 10
 
 
+def test_captured_calls_replay():
+    """Append, mass and eviction in one captured graph give what eager calls
+    give, replay after replay, beside a second graph with its own workspaces."""
+    rng = np.random.default_rng(17)
+    lens, H, k = [900, 300], 16, 128
+    pg = Paged(lens, seed=3)
+    _, (pool,), values = _latents("l4", rng, pg, 576)
+    q = bf16_cuda(to_bf16(rng.standard_normal((2, H, 576))))
+    sel = select(rng, lens, k)
+    idx = torch.from_numpy(sel).cuda()
+    cache, dims = pg.cache(), _dims(2, 512, 64, H, k)
+    keys = torch.zeros(pg.num_pages, 64, 32, dtype=torch.bfloat16, device="cuda")
+    new = bf16_cuda(to_bf16(rng.standard_normal((2, 576))))
+    key = bf16_cuda(to_bf16(rng.standard_normal((2, 32))))
+    lse = torch.full((2, H), 3.0, device="cuda")
+    start = torch.rand(2, 900, device="cuda")
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+
+    def buffers():
+        return dict(mass=torch.zeros(2, 900, device="cuda"), dst=torch.zeros(8, 64, 336, dtype=torch.uint8, device="cuda"),
+                    mass_dst=torch.zeros(2, 256, device="cuda"), lens=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                    kept=torch.zeros(2, 200, dtype=torch.int32, device="cuda"),
+                    ws=[dsa.l4_workspace(op, dims, cache) for op in
+                        (dsa.L4_OP_STATUS, dsa.L4_OP_ATTENTION_MASS, dsa.L4_OP_CACHE_EVICT)])
+
+    def call(b):
+        dsa.dsa_cache_append_l4(key, new, keys, pool, cache, dims, b["ws"][0])
+        dsa.dsa_attention_mass_l4(q, pool, cache, idx, lse, dims, 0.5, start, b["mass"], b["ws"][1])
+        dsa.dsa_cache_evict([(pool, b["dst"])], cache, dsa.Eviction(200, 4, 32), b["mass"], table,
+                            b["mass_dst"], b["lens"], b["kept"], b["ws"][2])
+
+    eager = buffers()
+    call(eager)
+    torch.cuda.synchronize()
+    graphs, bufs = [], [buffers(), buffers()]
+    torch.cuda.synchronize()
+    for b in bufs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(b)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for b in bufs:
+        for name in ("dst", "mass_dst", "lens", "kept"):
+            assert torch.equal(b[name], eager[name]), name
+        for r, n in enumerate(lens):
+            assert torch.equal(b["mass"][r, :n], eager["mass"][r, :n])
+
+
 def test_a_requests_life_over_the_4_bit_cache():
     """Prompt rows appended, attended, weighed; the cache evicted into fresh
     pages of the same pools; then decode steps on what is left: every stage

@@ -2,6 +2,10 @@
 byte against the float64 definition, sparse MLA over it (decode, prefill, the
 whole step) within bounds derived from its roundings."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +16,7 @@ from oracle import l4_oracle as l4
 from tests.l4_testutil import Paged, attention_bounds, bf16_cuda, random_l4, select, to_bf16
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _dims(n_q, W, P, *, topk=1, H=1, D_I=32, causal=0, q_pos0=0, scale=1.0, H_I=1):
@@ -172,7 +177,8 @@ SHAPES = [
     (32, 64, 512, 64, 512, 900), (150, 64, 512, 64, 130, 300), (7, 4, 64, 16, 256, 500),
     (5, 33, 448, 48, 300, 700), (4, 17, 192, 0, 65, 200), (2, 1, 128, 0, 64, 100),
     (1, 64, 512, 0, 4097, 6000), (6, 64, 320, 16, 1, 50), (2, 16, 512, 48, 63, 64),
-    (1, 64, 512, 64, 20000, 21000),
+    (1, 64, 512, 64, 20000, 21000), (3, 8, 64, 0, 70, 100), (2, 64, 256, 64, 1024, 2000),
+    (40, 64, 384, 32, 200, 400),
 ]
 
 
@@ -398,3 +404,151 @@ def test_forward_matches_definition(causal):
     dsa.dsa_attention_forward_l4(*args, None, out2, lse2, ws)
     torch.cuda.synchronize()
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_rows_without_context_and_a_4_byte_aligned_output():
+    """A sequence of length 0 in the batch, and results at addresses that are
+    only 4-byte aligned, with guard values around them."""
+    rng = np.random.default_rng(12)
+    for k, B in ((512, 3), (64, 160)):  # split rows and their merge; whole rows
+        lens = rng.integers(1, 600, B).tolist()
+        lens[1] = 0
+        pg = Paged(lens, seed=5)
+        pool, values = random_l4(rng, pg.num_pages, 576)
+        q = to_bf16(rng.standard_normal((B, 64, 576)))
+        idx = select(rng, lens, k)
+        cache, dims = pg.cache(), _dims(B, 576, 64, topk=k, H=64, scale=0.0625)
+        flat = torch.full((B * 64 * 512 + 2,), 5.0, device="cuda")
+        flat_lse = torch.full((B * 64 + 2,), 5.0, device="cuda")
+        out, lse = flat[1:-1].view(B, 64, 512), flat_lse[1:-1].view(B, 64)
+        assert out.data_ptr() % 16 == 4
+        ws = dsa.l4_workspace(dsa.L4_OP_SPARSE_MLA, dims, cache)
+        dsa.dsa_sparse_mla_decode_l4(bf16_cuda(q), torch.from_numpy(pool).cuda(), cache,
+                                     torch.from_numpy(idx).cuda(), dims, out, lse, ws)
+        assert dsa.workspace_check(ws) == (0, 0)
+        assert flat[0] == 5 and flat[-1] == 5 and flat_lse[0] == 5 and flat_lse[-1] == 5
+        rows = range(B) if B < 10 else (0, 1, 2, 77, 159)
+        _check_attention(q, values, pg, idx, out.double().cpu().numpy(), lse.double().cpu().numpy(),
+                         512, 0.0625, False, rows)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^31 bytes: rows at its end are written, read and attended."""
+    W, rb = 576, 336
+    pages = 2 ** 31 // (64 * rb) + 40
+    pool = torch.zeros(pages, 64, rb, dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(pages, 64, 32, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(2)
+    n = 128
+    x = to_bf16(rng.standard_normal((n, W)))
+    table = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32, device="cuda")
+    cache = dsa.PagedCache(torch.tensor([n], dtype=torch.int32, device="cuda"), table, pages, n)
+    dims = _dims(n, W, 64, causal=1)
+    ws = dsa.l4_workspace(dsa.L4_OP_STATUS, dims, cache)
+    dsa.dsa_cache_append_l4(torch.zeros(n, 32, dtype=torch.bfloat16, device="cuda"), bf16_cuda(x), keys,
+                            pool, cache, dims, ws)
+    values = l4.quantise(x)[1]
+    one = _dims(1, W, 64, topk=n, H=64, scale=0.0625)
+    idx = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    rows = torch.zeros(1, n, W, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_cache_read_l4(pool, cache, idx, one, rows, ws)
+    assert np.array_equal(rows[0].double().cpu().numpy(), values)
+    q = to_bf16(rng.standard_normal((1, 64, W)))
+    out, lse = torch.zeros(1, 64, 512, device="cuda"), torch.zeros(1, 64, device="cuda")
+    ws = dsa.l4_workspace(dsa.L4_OP_SPARSE_MLA, one, cache)
+    dsa.dsa_sparse_mla_decode_l4(bf16_cuda(q), pool, cache, idx, one, out, lse, ws)
+    assert dsa.workspace_check(ws) == (0, 0)
+    ref, ref_lse, p = l4.attention(q[0], values, 512, 0.0625)
+    tol, ltol = attention_bounds(q[0], values, 512, 0.0625, p)
+    assert (np.abs(out[0].double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - ref_lse) <= ltol).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls with workspaces of their own overlap without touching each other."""
+    rng = np.random.default_rng(15)
+    pg = Paged([1500] * 8, seed=4)
+    pool, _ = random_l4(rng, pg.num_pages, 576)
+    pool = torch.from_numpy(pool).cuda()
+    cache, dims = pg.cache(), _dims(8, 576, 64, topk=1024, H=64, scale=0.0625)
+    calls = []
+    for i in range(2):
+        q = bf16_cuda(to_bf16(rng.standard_normal((8, 64, 576))))
+        idx = torch.from_numpy(select(rng, pg.lens, 1024)).cuda()
+        calls.append((q, idx, torch.zeros(8, 64, 512, device="cuda"), torch.zeros(8, 64, device="cuda"),
+                      dsa.l4_workspace(dsa.L4_OP_SPARSE_MLA, dims, cache)))
+    alone = []
+    for q, idx, out, lse, ws in calls:
+        dsa.dsa_sparse_mla_decode_l4(q, pool, cache, idx, dims, out, lse, ws)
+        torch.cuda.synchronize()
+        alone.append((out.clone(), lse.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (q, idx, out, lse, ws), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                out.zero_()
+                dsa.dsa_sparse_mla_decode_l4(q, pool, cache, idx, dims, out, lse, ws)
+        torch.cuda.synchronize()
+        for (_, _, out, lse, _), (ref, ref_lse) in zip(calls, alone):
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("kernel", [8, 9], ids=["attention", "mass"])
+def test_bounded_wait_times_out(kernel):
+    """DSA_DEBUG_STALL makes the kernel wait once on a barrier that nothing
+    arrives at: with a 50 ms limit it reports a time-out, drains what is in
+    flight and returns, and the context stays usable (in a child process: the
+    library reads both variables once)."""
+    code = r"""
+import sys, numpy as np, torch
+sys.path.insert(0, %r)
+import sparse_attention_scores_b200 as dsa
+from tests.l4_testutil import Paged, bf16_cuda, random_l4, select
+rng = np.random.default_rng(0)
+pg = Paged([3000, 1500], seed=1)
+pool, _ = random_l4(rng, pg.num_pages, 576)
+cache = pg.cache()
+dims = dsa.Dims(2, 1, 32, 2048, 64, 512, 64, 0, 0, 0.0625)
+pool, q = torch.from_numpy(pool).cuda(), bf16_cuda(rng.standard_normal((2, 64, 576)))
+idx = torch.from_numpy(select(rng, pg.lens, 2048)).cuda()
+out, lse = torch.zeros(2, 64, 512, device="cuda"), torch.zeros(2, 64, device="cuda")
+if %d == 8:
+    ws = dsa.l4_workspace(dsa.L4_OP_SPARSE_MLA, dims, cache)
+    dsa.dsa_sparse_mla_decode_l4(q, pool, cache, idx, dims, out, lse, ws)
+else:
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    mass = torch.zeros(2, 3000, device="cuda")
+    dsa.dsa_attention_mass_l4(q, pool, cache, idx, lse, dims, 1.0, mass, mass, ws)
+st, info = dsa.workspace_check(ws)
+x = torch.ones(1000, device="cuda").sum().item()
+print("STATUS", st, hex(info), x)
+""" % (ROOT, kernel)
+    env = dict(os.environ, DSA_WAIT_LIMIT_NS="50000000", DSA_DEBUG_STALL=str(kernel))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env,
+                         timeout=300, cwd=ROOT)
+    assert res.returncode == 0, res.stderr[-2000:]
+    line = [ln for ln in res.stdout.splitlines() if ln.startswith("STATUS")][0].split()
+    assert int(line[1]) == 5 and int(line[2], 16) >> 24 == kernel and line[3] == "1000.0", line
+
+
+def test_binding_checks_types_and_layouts():
+    pg = Paged([100], seed=1)
+    cache, dims = pg.cache(), _dims(1, 80, 16, topk=8, H=4)
+    pool = torch.zeros(pg.num_pages, 64, 48, dtype=torch.uint8, device="cuda")
+    q = torch.zeros(1, 4, 80, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros(1, 4, 64, device="cuda"), torch.zeros(1, 4, device="cuda")
+    ws = dsa.l4_workspace(dsa.L4_OP_SPARSE_MLA, dims, cache)
+    good = dict(q=q, latent4_pages=pool, idx=idx, out=out, lse=lse)
+    for name, bad in (("q", q.float()), ("q", q.cpu()), ("q", q[:, :3]), ("idx", idx.long()),
+                      ("latent4_pages", pool[:, :, :40]), ("latent4_pages", pool[:-1]),
+                      ("out", torch.zeros(1, 64, 4, device="cuda").transpose(1, 2)),
+                      ("lse", lse.double())):
+        a = dict(good, **{name: bad})
+        with pytest.raises(ValueError, match=name):
+            dsa.dsa_sparse_mla_decode_l4(a["q"], a["latent4_pages"], cache, a["idx"], dims, a["out"],
+                                         a["lse"], ws)
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_sparse_mla_prefill_l4(q, pool, cache, idx, dims, out, lse, ws)  # decode dims
+    dsa.dsa_sparse_mla_decode_l4(q, pool, cache, idx, dims, out, lse, ws)
+    assert dsa.workspace_check(ws) == (0, 0)
