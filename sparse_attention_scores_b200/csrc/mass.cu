@@ -72,7 +72,13 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
 
 
 // Shared memory: two slots of the tile (64 keys x W), the query tile, barriers.
-constexpr int kMisc = 1536;
+// Tensor memory: kParts partial sums of S per slot, which the reader adds.  The
+// tensor cores truncate each accumulation towards zero, and the errors of a
+// chain add up in the logit: 512 causal rows of 2,048 keys are off by 1.4e-6
+// with one chain of 36 (340 us), 6.5e-7 with two of 18 (349 us), 3.4e-7 with
+// four (361 us); fp32 additions give 6e-8.
+constexpr int kMisc = 2048;
+constexpr int kParts = 2;
 struct Layout {
   int nQ;
   uint32_t slot, off_q, off_misc, bytes;
@@ -105,8 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
   uint64_t *full = bars;         // [2] slot filled (one arrive per filling warp)
-  uint64_t *empty = bars + 2;    // [2] S and key factors read (one arrive per summing warp)
-  uint64_t *sfull = bars + 4;    // [2] S in tensor memory (MMA commit)
+  uint64_t *sread = bars + 2;    // [2] S read (one arrive per summing warp)
+  uint64_t *sfull = bars + 4;    // [2] S in tensor memory, the slot's tile free (MMA commit)
   uint64_t *rowfull = bars + 6;  // [2] the slot's pool rows known (row warp)
   uint64_t *rowfree = bars + 8;  // [2] and read (one arrive per filling warp)
   uint64_t *qready = bars + 10;
@@ -116,8 +122,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 14);
   volatile uint32_t *failed = misc + 1;
   float *qmax = reinterpret_cast<float *>(bars + 16);      // [13], padded to 16
-  float *factor = qmax + 16;                               // [2][64] a key's scale, +inf: unused
-  int *rowi = reinterpret_cast<int *>(factor + 2 * kKeys);  // [2][64] pool row, -1: none
+  // [4][64] a key's scale, +inf: unused.  Four slots: the tile of slot j + 4 is
+  // filled after S of slot j + 2, which is formed after S of slot j was read
+  float *factor = qmax + 16;
+  int *rowi = reinterpret_cast<int *>(factor + 4 * kKeys);  // [2][64] pool row, -1: none
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int split = blockIdx.x;
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&full[s], kWideWarps);
-      mbar_init(&empty[s], kSoftWarps);
+      mbar_init(&sread[s], kSoftWarps);
       mbar_init(&sfull[s], 1);
       mbar_init(&rowfull[s], 1);
       mbar_init(&rowfree[s], kWideWarps);
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(const_cast<uint32_t *>(&misc[0]), 2 * kKeys);
+    tmem_alloc(const_cast<uint32_t *>(&misc[0]), 2 * kParts * kHeads);
     tmem_relinquish();
   }
   // What this kernel reads is older than decay_kernel, which had waited for it
@@ -200,12 +208,20 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       const int next[2] = {place(j + 1, 0), place(j + 1, 1)};
       tc_fence_after();
       uint32_t v[32];
-      tmem_ld_16x256b_x8(tmem + lane_off + kKeys * s, v);
-      const float f0 = factor[s * kKeys + k0], f1 = factor[s * kKeys + k0 + 8];
+      tmem_ld_16x256b_x8(tmem + lane_off + s * kParts * kHeads, v);
+      const float f0 = factor[(j & 3) * kKeys + k0], f1 = factor[(j & 3) * kKeys + k0 + 8];
       tmem_ld_wait();
+      for (int x = 1; x < min(kParts, lay.nQ); ++x) {
+        uint32_t u[32];
+        tmem_ld_16x256b_x8(tmem + lane_off + (s * kParts + x) * kHeads, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0) mbar_arrive(&sread[s]);
       const float t0 = f0 * zscale, t1 = f1 * zscale;
       float w0 = 0.f, w1 = 0.f;
 #pragma unroll
@@ -243,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       r_of[i] = r < kKeys ? r : -1;
       u_of[i] = static_cast<int>(t) - r * units;
     }
-    auto set_factor = [&](int s, int r, bool live, float f) {
-      factor[s * kKeys + r] = live ? f : INFINITY;
+    auto set_factor = [&](int j, int r, bool live, float f) {
+      factor[(j & 3) * kKeys + r] = live ? f : INFINITY;
     };
     if constexpr (F == kLatBf16) {
       // straight into the tile, one slot behind the one being waited for
@@ -252,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
         const int s = j & 1;
         if (j < nh) {
           if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) break;
-          if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+          if (j >= 2 && !wait_or_fail(&sfull[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
 #pragma unroll
           for (int i = 0; i < kT; ++i) {
             if (r_of[i] < 0) continue;
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
             const uint8_t *src = p.latent + static_cast<int64_t>(max(at, 0)) * bytes + 16 * u;
             cp_async_16(tile + s * lay.slot + (u >> 3) * kAtom + r * 128 + (((u & 7) ^ (r & 7)) << 4),
                         src, at >= 0 ? 16u : 0u);
-            if (u == 0) set_factor(s, r, at >= 0, 1.f);
+            if (u == 0) set_factor(j, r, at >= 0, 1.f);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&rowfree[s]);
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       bool loaded = nh > 0 && load_rows(0);
       for (int j = 0; j < nh && loaded; ++j) {
         const int s = j & 1;
-        if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+        if (j >= 2 && !wait_or_fail(&sfull[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
 #pragma unroll
         for (int i = 0; i < kT; ++i) {
           if (r_of[i] < 0) continue;
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
             }
           }
           if (u == 0)
-            set_factor(s, r, live, F == kLatL4 ? pow2i(l4_exponent(__float_as_uint(ef[i]))) : ef[i]);
+            set_factor(j, r, live, F == kLatL4 ? pow2i(l4_exponent(__float_as_uint(ef[i]))) : ef[i]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -391,19 +407,24 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     for (int j = 0; j < nh && ok; ++j) {
       const int s = j & 1;
       if (!__all_sync(0xffffffffu, wait_or_fail(&full[s], (j >> 1) & 1, p.wait_ns, failed))) break;
+      if (j >= 2 && !__all_sync(0xffffffffu, wait_or_fail(&sread[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)))
+        break;
       fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t d = tm + kKeys * s;
+      const uint32_t d = tm + s * kParts * kHeads;
       const uint64_t d_l = smem_desc(tile_u + s * lay.slot, 16, 1024, kLayoutSW128);
-#pragma unroll 3
+      // 64-column atom a adds to partial sum a % kParts
+#pragma unroll 4
       for (int a = 0; a < full_atoms; ++a)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f16_elect(d, d_l + ((a * kAtom + k * 32) >> 4), d_q + ((a * kAtom + k * 32) >> 4),
-                        idesc, (a | k) != 0 ? 1u : 0u);
+          mma_f16_elect(d + (a & (kParts - 1)) * kHeads, d_l + ((a * kAtom + k * 32) >> 4),
+                        d_q + ((a * kAtom + k * 32) >> 4), idesc, a >= kParts || k != 0 ? 1u : 0u);
       for (int k = 0; k < tail; ++k)
-        mma_f16_elect(d, d_l + ((full_atoms * kAtom + k * 32) >> 4),
-                      d_q + ((full_atoms * kAtom + k * 32) >> 4), idesc, (full_atoms | k) != 0 ? 1u : 0u);
+        mma_f16_elect(d + (full_atoms & (kParts - 1)) * kHeads,
+                      d_l + ((full_atoms * kAtom + k * 32) >> 4),
+                      d_q + ((full_atoms * kAtom + k * 32) >> 4), idesc,
+                      full_atoms >= kParts || k != 0 ? 1u : 0u);
       commit_elect(&sfull[s]);
     }
     if (*failed) {
@@ -418,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   if (*failed && tid == 0) report(p.status, kErrTimeout, (kKernMass << 24) | 1u);
   if (warp == kMmaWarp) {
     __syncwarp();
-    tmem_dealloc(tmem, 2 * kKeys);
+    tmem_dealloc(tmem, 2 * kParts * kHeads);
   }
 }
 
