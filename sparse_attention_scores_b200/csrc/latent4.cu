@@ -7,12 +7,11 @@
 //   v    = e2m1(x / (s[b] * 2^e))
 // x has 8 significant bits, s 4 and every boundary between two e2m1 codes 3, so
 // a boundary times s fits 8 bits too: a quotient that is not a boundary differs
-// from it by 2^-8 or more, relative.  So the quotient is taken as x times the
-// block's reciprocal (off by 2^-22 at most) and rounded to fp16 (2^-12), which
-// puts a quotient that is a boundary back onto it and moves none across: the
-// codes are those of the exact quotients, without a division per column.  (The
-// scales' divisions are IEEE fp32 ones; E4M3's boundaries have 5 bits, so the
-// same argument holds for them.)
+// from it by 2^-8 or more, relative.  So the quotient is taken as x times an
+// approximate reciprocal (2^-21) and rounded to fp16 (2^-12), which puts a
+// quotient that is a boundary back onto it and moves none across: the codes are
+// those of the exact quotients, without an exact division.  The same holds for
+// the scale, whose boundaries have 5 bits, 7 times 6.
 //
 // A warp takes one row, a lane a 16-byte piece of 8 columns (72 pieces at
 // W = 576, three rounds), two lanes a block.  Both kernels move each byte once;
@@ -95,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const int c = lane + 32 * i;
-    const uint32_t code = f32_to_e4m3(bmax[i] * inv / 6.f);
+    const uint32_t code = f16_to_e4m3(__float2half_rn(fminf(bmax[i] * inv * (1.f / 6.f), 448.f)));
     const float s = __low2float(e4m3_to_half2(code));
-    const float rs = s > 0.f ? inv / s : 0.f;  // a block whose scale is 0 is stored as zeros
+    const float rs = s > 0.f ? __fdividef(inv, s) : 0.f;  // a block whose scale is 0 is stored as zeros
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t out = 0u;
 #pragma unroll

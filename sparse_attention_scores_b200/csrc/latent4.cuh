@@ -82,9 +82,10 @@ __device__ __forceinline__ int l4_row_exponent(float amax) {
   return max(-kL4MaxExp, min(kL4MaxExp, e));
 }
 // E4M3 code of x >= 0, round to nearest even, saturating
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+__device__ __forceinline__ uint32_t f16_to_e4m3(__half x) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  const uint32_t two = __half_as_ushort(x);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(two));
   return r & 0xFFu;
 }
 // two e2m1 codes, a in the low nibble, round to nearest even, saturating

@@ -75,8 +75,8 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
 // Tensor memory: kParts partial sums of S per slot, which the reader adds.  The
 // tensor cores truncate each accumulation towards zero, and the errors of a
 // chain add up in the logit: 512 causal rows of 2,048 keys are off by 1.4e-6
-// with one chain of 36 (340 us), 6.5e-7 with two of 18 (349 us), 3.4e-7 with
-// four (361 us); fp32 additions give 6e-8.
+// with one chain of 36, 6.5e-7 with two of 18 (3% slower), 3.4e-7 with four (6%);
+// fp32 additions give 6e-8.
 constexpr int kMisc = 2048;
 constexpr int kParts = 2;
 struct Layout {
@@ -100,6 +100,14 @@ __host__ __device__ constexpr int units_of(int W) {
 }
 template <int F>
 constexpr int kTasksOf = (2 * units_of<F>(576) + kWideWarps - 1) / kWideWarps;
+// Warps that fill a slot.  bf16 rows are copied, which takes no registers: four
+// warps fill the even slots and four the odd ones, so that a slot is announced
+// when its own copies have landed (with one group for both, one slot's copies
+// were issued between another's arrival and its announcement: 349 us against
+// 266 for 512 causal rows of 2,048 keys).  What is left is the copies' own rate,
+// about 17 bytes a cycle and SM.
+template <int F>
+constexpr int kFillers = F == kLatBf16 ? 4 : kWideWarps;
 
 template <int F>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
@@ -132,11 +140,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   const int row = p.rows.causal ? p.n_q - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&full[s], kWideWarps);
+      mbar_init(&full[s], kFillers<F>);
       mbar_init(&sread[s], kSoftWarps);
       mbar_init(&sfull[s], 1);
       mbar_init(&rowfull[s], 1);
-      mbar_init(&rowfree[s], kWideWarps);
+      mbar_init(&rowfree[s], kFillers<F>);
     }
     mbar_init(qready, kSoftWarps + kWideWarps);
     mbar_init(bar_drain, 1);
@@ -247,50 +255,45 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     // ----------------------------------------------------------------- filling
     // A slot's 64 x units 16-byte units, 32 neighbours per task: coalesced, and
     // eight neighbouring lanes store to eight different 16-byte columns
-    constexpr int kT = kTasksOf<F>;
     const int g = warp == kLastWideWarp ? kWideWarps - 1 : warp - kSoftWarps;
     const int units = units_of<F>(W), nb = W / kL4Block;
     const int bytes = F == kLatBf16 ? 2 * W : (F == kLatE4m3 ? W : l4_row_bytes(W));
-    int r_of[kT], u_of[kT];  // row -1: no unit
-#pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      const uint32_t t = static_cast<uint32_t>((g + kWideWarps * i) * 32 + lane);
-      const int r = static_cast<int>((t * p.units_inv) >> 20);
-      r_of[i] = r < kKeys ? r : -1;
-      u_of[i] = static_cast<int>(t) - r * units;
-    }
     auto set_factor = [&](int j, int r, bool live, float f) {
       factor[(j & 3) * kKeys + r] = live ? f : INFINITY;
     };
     if constexpr (F == kLatBf16) {
-      // straight into the tile, one slot behind the one being waited for
-      for (int j = 0; j <= nh; ++j) {
+      for (int j = g >> 2; j < nh && g < 2 * kFillers<F>; j += 2) {
         const int s = j & 1;
-        if (j < nh) {
-          if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) break;
-          if (j >= 2 && !wait_or_fail(&sfull[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
-#pragma unroll
-          for (int i = 0; i < kT; ++i) {
-            if (r_of[i] < 0) continue;
-            const int r = r_of[i], u = u_of[i], at = rowi[s * kKeys + r];
-            const uint8_t *src = p.latent + static_cast<int64_t>(max(at, 0)) * bytes + 16 * u;
-            cp_async_16(tile + s * lay.slot + (u >> 3) * kAtom + r * 128 + (((u & 7) ^ (r & 7)) << 4),
-                        src, at >= 0 ? 16u : 0u);
-            if (u == 0) set_factor(j, r, at >= 0, 1.f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rowfree[s]);
+        if (!wait_or_fail(&rowfull[s], (j >> 1) & 1, p.wait_ns, failed)) break;
+        if (j >= 2 && !wait_or_fail(&sfull[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
+#pragma unroll 6
+        for (int t = (g & 3) * 32 + lane; t < kKeys * units; t += 32 * kFillers<F>) {
+          const int r = static_cast<int>((static_cast<uint32_t>(t) * p.units_inv) >> 20);
+          const int u = t - r * units, at = rowi[s * kKeys + r];
+          const uint8_t *src = p.latent + static_cast<int64_t>(max(at, 0)) * bytes + 16 * u;
+          cp_async_16(tile + s * lay.slot + (u >> 3) * kAtom + r * 128 + (((u & 7) ^ (r & 7)) << 4), src,
+                      at >= 0 ? 16u : 0u);
+          if (u == 0) set_factor(j, r, at >= 0, 1.f);
         }
         cp_async_commit();
-        if (j > 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s ^ 1]);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rowfree[s]);
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
       }
       cp_async_wait_all();
     } else {
+      constexpr int kT = kTasksOf<F>;
+      int r_of[kT], u_of[kT];  // row -1: no unit
+#pragma unroll
+      for (int i = 0; i < kT; ++i) {
+        const uint32_t t = static_cast<uint32_t>((g + kWideWarps * i) * 32 + lane);
+        const int r = static_cast<int>((t * p.units_inv) >> 20);
+        r_of[i] = r < kKeys ? r : -1;
+        u_of[i] = static_cast<int>(t) - r * units;
+      }
       uint4 data[kT];
       uint32_t sc[kT];  // 4-bit rows: the unit's two block scales
       float ef[kT];     // the row's factor (for unit 0)
