@@ -187,7 +187,7 @@ typedef struct {
  *   mass      [num_seqs, mass_ld] fp32, mass_ld >= max_seq_len
  *   mass_dst  [num_seqs, mass_dst_ld] fp32, mass_dst_ld >= min(budget,
  *             max_seq_len); may be NULL; must not overlap mass
- *   new_lens  [num_seqs] int32 output
+ *   new_lens  [num_seqs] int32 output; may be cache->seq_lens
  *   kept      [num_seqs, budget] int32 output: the kept positions, ascending,
  *             -1 padded; may be NULL
  * Destination rows, masses and pages past new_lens[b] are left untouched.  A

@@ -45,10 +45,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const EvictParams p) {
   griddep_launch_dependents();
   const int b = blockIdx.y;
   const int n = max(0, min(p.seq_lens[b], p.max_len));
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.lens[b] = n;
-    p.new_lens[b] = min(n, p.budget);
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.lens[b] = n;
   for (int s = blockIdx.x * kThreads + threadIdx.x; s < n; s += gridDim.x * kThreads) {
     const float m = p.mass[b * p.mass_ld + s];
     float v = (m != m) ? -INFINITY : fminf(m, FLT_MAX);
@@ -94,6 +91,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) 
   griddep_launch_dependents();
   const int b = blockIdx.y, lane = lane_id();
   const int n = min(p.lens[b], p.budget);
+  // not in rank_kernel: new_lens may be seq_lens, which all its CTAs read
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.new_lens[b] = n;
   const int step = gridDim.x * (kThreads / 32) * kRows;
   for (int i0 = (blockIdx.x * (kThreads / 32) + warp_id()) * kRows; i0 < n; i0 += step) {
     const int i = i0 + lane;

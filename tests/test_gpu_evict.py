@@ -239,6 +239,30 @@ def test_evict_reports_pages_out_of_range():
     assert st[0] == 6 and st[1] >> 24 == 10
 
 
+def test_evict_updates_the_lengths_in_place():
+    """new_lens may be the cache's own seq_lens, which every part of the ranking
+    reads; a call that moves neither masses nor positions out gives the same rows."""
+    rng = np.random.default_rng(23)
+    lens = [30000, 50, 9000, 30001]
+    pg = Paged(lens, seed=9)
+    mass = torch.from_numpy(_masses(rng, 4, max(lens), "plain")).cuda()
+    pool = torch.from_numpy(rng.integers(0, 256, (pg.num_pages, 64, 336)).astype(np.uint8)).cuda()
+    table = torch.arange(32, dtype=torch.int32, device="cuda").view(4, 8)
+    out = []
+    for in_place in (False, True):
+        cache, dst = pg.cache(), torch.zeros(32, 64, 336, dtype=torch.uint8, device="cuda")
+        lens_out = cache.seq_lens if in_place else torch.zeros(4, dtype=torch.int32, device="cuda")
+        ws = dsa.l4_workspace(dsa.L4_OP_CACHE_EVICT, None, cache)
+        kept = None if in_place else torch.zeros(4, 500, dtype=torch.int32, device="cuda")
+        mass_dst = None if in_place else torch.zeros(4, 500, device="cuda")
+        dsa.dsa_cache_evict([(pool, dst)], cache, dsa.Eviction(500, 4, 100), mass, table, mass_dst,
+                            lens_out, kept, ws)
+        assert dsa.workspace_check(ws) == (0, 0)
+        out.append((dst, lens_out.tolist()))
+    assert out[0][1] == out[1][1] == [500, 50, 500, 500]
+    assert torch.equal(out[0][0], out[1][0])
+
+
 def test_captured_calls_replay():
     """Append, mass and eviction in one captured graph give what eager calls
     give, replay after replay, beside a second graph with its own workspaces."""
