@@ -6,7 +6,8 @@
  * asynchronous on `stream` (NULL: the per-thread default stream), host checks
  * before any launch with no side effects on refusal, device-side range checks
  * that skip the access and are read back with dsa_workspace_check(), and a
- * workspace that serves one call at a time.
+ * workspace that serves one call at a time.  A block table has at most
+ * 2^25 - 1 pages per sequence (DSA_ERR_UNSUPPORTED).
  *
  * Row format ("l4")
  * -----------------

@@ -43,6 +43,12 @@ int64_t scores_ld(const dsa_dims_t &d, const dsa_cache_t &c) {
   return std::max<int64_t>(4, (max_keys(d, c) + 3) & ~static_cast<int64_t>(3));
 }
 
+// check_cache, and positions that fit 32 bits up to the block table's last slot
+dsa_status_t check_cache_l4(const dsa_cache_t *c, const dsa_dims_t &d) {
+  DSA_TRY(check_cache(c, d));
+  return c->max_pages > INT32_MAX / kPageSize ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
 PagedRows paged(const dsa_cache_t &c, const dsa_dims_t &d) {
   return PagedRows{c.seq_lens, c.block_table, c.max_pages, c.num_pages, d.causal, d.q_pos0};
 }
@@ -53,7 +59,7 @@ int64_t evict_rank_ld(const dsa_cache_t &c) {
 dsa_status_t check_evict_cache(const dsa_cache_t *c) {
   dsa_dims_t d = {};
   if (c != nullptr) d.n_q = c->num_seqs;
-  DSA_TRY(check_cache(c, d));
+  DSA_TRY(check_cache_l4(c, d));
   return c->num_seqs > 65535 ? DSA_ERR_UNSUPPORTED : DSA_OK;  // grid.y
 }
 
@@ -106,7 +112,7 @@ dsa_status_t mla4_entry(const uint16_t *q, const uint8_t *latent, const dsa_cach
   DSA_TRY(check_dims_common(dims));
   if (dims->causal != want_causal) return DSA_ERR_INVALID_ARG;
   DSA_TRY(check_mla_dims(*dims));
-  DSA_TRY(check_cache(cache, *dims));
+  DSA_TRY(check_cache_l4(cache, *dims));
   if (q == nullptr || latent == nullptr || idx == nullptr || out == nullptr || lse == nullptr)
     return DSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(latent, 16) || !aligned(idx, 4) || !aligned(out, 4) ||
@@ -125,7 +131,7 @@ dsa_status_t mass_entry(LatentFormat format, const uint16_t *q, const void *late
                         dsa_stream_t stream) {
   DSA_TRY(check_dims_common(dims));
   DSA_TRY(check_mla_dims(*dims));
-  DSA_TRY(check_cache(cache, *dims));
+  DSA_TRY(check_cache_l4(cache, *dims));
   if (q == nullptr || latent == nullptr || idx == nullptr || lse == nullptr || mass_out == nullptr ||
       (format == kLatE4m3 && lat_scale == nullptr))
     return DSA_ERR_INVALID_ARG;
@@ -179,7 +185,7 @@ size_t dsa_l4_workspace_bytes(dsa_l4_op_t op, const dsa_dims_t *dims, const dsa_
   if (check_dims_common(dims) != DSA_OK) return 0;
   if (op == DSA_L4_OP_STATUS) return kStatusBytes;
   if (check_mla_dims(*dims) != DSA_OK) return 0;
-  if (op == DSA_L4_OP_ATTENTION_FORWARD && check_cache(cache, *dims) != DSA_OK) return 0;
+  if (op == DSA_L4_OP_ATTENTION_FORWARD && check_cache_l4(cache, *dims) != DSA_OK) return 0;
   return ws_bytes_for(op, *dims, cache ? *cache : dsa_cache_t{});
 }
 
@@ -191,7 +197,7 @@ dsa_status_t dsa_cache_append_l4(const uint16_t *k_idx_new, const uint16_t *late
   const dsa_dims_t &d = *dims;
   if (d.D_I != 32 && d.D_I != 64 && d.D_I != 128) return DSA_ERR_UNSUPPORTED;
   DSA_TRY(check_row(d.R, d.P));
-  DSA_TRY(check_cache(cache, d));
+  DSA_TRY(check_cache_l4(cache, d));
   if (k_idx_new == nullptr || latent_new == nullptr || k_idx_pages == nullptr ||
       latent4_pages == nullptr)
     return DSA_ERR_INVALID_ARG;
@@ -220,7 +226,7 @@ dsa_status_t dsa_cache_read_l4(const uint8_t *latent4_pages, const dsa_cache_t *
   const dsa_dims_t &d = *dims;
   DSA_TRY(check_row(d.R, d.P));
   if (d.topk < 1) return DSA_ERR_INVALID_ARG;
-  DSA_TRY(check_cache(cache, d));
+  DSA_TRY(check_cache_l4(cache, d));
   if (latent4_pages == nullptr || idx == nullptr || rows == nullptr) return DSA_ERR_INVALID_ARG;
   if (!aligned(latent4_pages, 16) || !aligned(idx, 4) || !aligned(rows, 16))
     return DSA_ERR_INVALID_ARG;
@@ -259,7 +265,7 @@ dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float *w,
                                       float *lse, void *ws, size_t ws_bytes, dsa_stream_t stream) {
   DSA_TRY(check_dims_common(dims));
   DSA_TRY(check_mla_dims(*dims));
-  DSA_TRY(check_cache(cache, *dims));
+  DSA_TRY(check_cache_l4(cache, *dims));
   if (q == nullptr || latent4_pages == nullptr || out == nullptr || lse == nullptr)
     return DSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(latent4_pages, 16) || !aligned(out, 4) || !aligned(lse, 4) ||

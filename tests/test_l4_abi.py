@@ -162,6 +162,21 @@ def test_evict_refuses(L):
     assert call(ws=1024) == 4
 
 
+def test_block_tables_past_32_bit_positions_are_refused(L):
+    _host_only()
+    for pages, st in ((2 ** 25, 2), (2 ** 25 - 1, 4)):  # the second passes on to the workspace check
+        c = _cache(max_pages=pages)
+        d, p = _dims(), _dims(causal=1)
+        assert L.dsa_cache_append_l4(A, A, A, A, c, d, WS, 16, None) == st
+        assert L.dsa_cache_read_l4(A, c, A, d, A, WS, 16, None) == st
+        assert L.dsa_sparse_mla_decode_l4(A, A, c, A, d, A, A, WS, 16, None) == st
+        assert L.dsa_sparse_mla_prefill_l4(A, A, c, A, p, A, A, WS, 16, None) == st
+        assert L.dsa_attention_forward_l4(A, A, A, A, A, c, d, A, A, A, WS, 16, None) == st
+        assert L.dsa_attention_mass_l4(A, A, c, A, A, d, 1.0, A, A, 256, WS, 16, None) == st
+        e = latent4.EvictStruct(128, 0, 0, 0x600000, 2, 8)
+        assert L.dsa_cache_evict(None, 0, c, ctypes.byref(e), A, 256, A, 128, A, None, WS, 16, None) == st
+
+
 def test_binding_refuses_what_a_pointer_cannot_carry():
     """Strides, types and devices are checked before the library is called."""
     import torch
