@@ -124,10 +124,11 @@ DSA_API dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float
  *   lse       [n_q, H] fp32, the step's; a row with lse = -inf adds nothing
  *   decay     finite, >= 0
  *   mass_in   [num_seqs, mass_ld] fp32, or NULL for zeros
- *   mass_out  [num_seqs, mass_ld] fp32; may be mass_in.  Entries s < len(b) are
- *             written (len(b): seq_lens[b], for a causal chunk q_pos0 + n_q,
- *             at most mass_ld); entries past that are left untouched.
- *             mass_ld >= the longest len
+ *   mass_out  [num_seqs, mass_ld] fp32; may be mass_in, else apart from it.  Entries s < len(b) are
+ *             written (len(b): seq_lens[b], at most max_seq_len; for a causal
+ *             chunk q_pos0 + n_q); entries past that are left untouched, and
+ *             so is everything when n_q = 0.  mass_ld >= max_seq_len, for a
+ *             causal chunk >= q_pos0 + n_q
  * A position that a row holds twice counts twice.  Causal chunks add their
  * rows in 64-bit fixed point (steps of 2^-40), so the result does not depend
  * on the order in which the rows ran; a decode row adds in fp32, once per

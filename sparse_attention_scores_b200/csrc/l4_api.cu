@@ -155,6 +155,7 @@ dsa_status_t mass_entry(LatentFormat format, const uint16_t *q, const void *late
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.mass_ld = mass_ld;
+  a.max_len = static_cast<int>(max_keys(*dims, *cache));
   a.n_q = dims->n_q;
   a.num_seqs = cache->num_seqs;
   a.H = dims->H;

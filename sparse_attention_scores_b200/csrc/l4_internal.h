@@ -73,6 +73,7 @@ struct MassLaunch {
   const float *mass_in;
   float *mass_out;
   int64_t mass_ld;
+  int max_len;  // a sequence's length counts up to this one (<= mass_ld)
   int n_q, num_seqs, H, R, P, topk;
   float scale, decay;
   void *scratch;  // causal chunks: 64-bit sums [q_pos0 + n_q]

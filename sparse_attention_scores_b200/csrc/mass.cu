@@ -34,6 +34,7 @@ struct MassParams {
   float *mass_out;
   unsigned long long *fixed;
   int64_t mass_ld;
+  int max_len;
   int n_q, num_seqs, H, W, topk, nsplit;
   uint32_t cpr_inv, units_inv;  // inverses of 16-byte pieces per query head and per stored row, at 2^20
   float scale_log2, decay;
@@ -42,10 +43,10 @@ struct MassParams {
   DevStatus *status;
 };
 
-// tokens of sequence b whose mass is kept, at most the row stride
+// tokens of sequence b, at most max_len
 __device__ __forceinline__ int mass_len(const MassParams &p, int b) {
   const int len = p.rows.causal ? p.rows.q_pos0 + p.n_q : p.rows.seq_lens[b];
-  return static_cast<int>(min(static_cast<int64_t>(max(0, len)), p.mass_ld));
+  return max(0, min(len, p.max_len));
 }
 
 __global__ void __launch_bounds__(kSweep) decay_kernel(const MassParams p) {
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kSweep) decay_kernel(const MassParams p) {
 
 // one row's weight of one kept position
 __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos, float w) {
-  if (pos < 0 || pos >= p.mass_ld) return;
+  if (pos < 0 || pos >= p.max_len) return;
   if (p.rows.causal)
     atomicAdd(&p.fixed[pos], static_cast<unsigned long long>(
                                  __double2ll_rn(static_cast<double>(w) * kFixedOne)));
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     if (tid == 0 && !mbar_wait(bar_stall, 0u, p.wait_ns)) *failed = 1u;
     __syncthreads();
   }
-  const int len = l4_row_len(p.rows, row), limit = l4_limit(p.rows, len);
+  const int len = min(l4_row_len(p.rows, row), p.max_len), limit = l4_limit(p.rows, len);
   const int nsel = max(0, min(p.topk, len));
   const int nh_row = (nsel + kKeys - 1) / kKeys;
   const int per = (nh_row + p.nsplit - 1) / p.nsplit;
@@ -489,6 +490,7 @@ dsa_status_t launch_mass(const MassLaunch &a, cudaStream_t stream) {
   p.mass_out = a.mass_out;
   p.fixed = a.rows.causal ? static_cast<unsigned long long *>(a.scratch) : nullptr;
   p.mass_ld = a.mass_ld;
+  p.max_len = a.max_len;
   p.n_q = a.n_q;
   p.num_seqs = a.num_seqs;
   p.H = a.H;

@@ -123,6 +123,13 @@ def _on(stream, device):
     return _dsa._stream(stream)
 
 
+def _row_stride(t, seqs, need):
+    """Elements between the rows of a [sequences, positions] tensor.  The library
+    checks it against the `need` positions it may touch, so a tensor that is
+    narrower than that states its width."""
+    return t.stride(0) if seqs > 1 and t.shape[1] >= need else t.shape[1]
+
+
 def _pool4(t, device, cache, dims):
     """A pool of 4-bit rows.  For an unsupported R or P any row width passes, so
     that the library's refusal is the one that is raised."""
@@ -233,9 +240,9 @@ def _mass(where, q, latent, cache, idx, lse, dims, decay, mass_in, mass_out, ws,
     seqs = cache.seq_lens.shape[0]
     if mass_out.dim() != 2 or mass_out.shape[0] != seqs:
         raise ValueError("mass_out: not [sequences, positions]")
-    ld = mass_out.stride(0) if seqs > 1 else mass_out.shape[1]
+    ld = _row_stride(mass_out, seqs, dims.q_pos0 + dims.n_q if dims.causal else cache.max_seq_len)
     if mass_in is not None and (mass_in.shape != mass_out.shape or
-                                (seqs > 1 and mass_in.stride(0) != ld)):
+                                (seqs > 1 and mass_in.stride(0) != mass_out.stride(0))):
         raise ValueError("mass_in: not laid out as mass_out")
     status = getattr(_ready, where)(
         _arg(q, "q", _bf16, dev, (dims.n_q, dims.H, dims.R + dims.P)), *latent, c,
@@ -320,14 +327,13 @@ def dsa_cache_evict(pools, cache, evict: Eviction, mass, dst_block_table, mass_d
     for name, t in (("mass", mass), ("mass_dst", mass_dst)):
         if t is not None and (t.dim() != 2 or t.shape[0] != seqs):
             raise ValueError(f"{name}: not [sequences, positions]")
-    wide = 0 if seqs > 1 else 1  # row stride, or the width of a single row
     e = EvictStruct(evict.budget, evict.sinks, evict.recent,
                     _arg(dst_block_table, "dst_block_table", _i32, dev), dst_block_table.shape[1],
                     dst_pages if dst_pages is not None else 1 << 24)
     status = L.dsa_cache_evict(
         arr, len(pools), c, _byref(e), _arg(mass, "mass", _f32, dev, rows=True),
-        mass.shape[1] if wide else mass.stride(0), _arg(mass_dst, "mass_dst", _f32, dev, rows=True),
-        0 if mass_dst is None else mass_dst.shape[1] if wide else mass_dst.stride(0),
+        _row_stride(mass, seqs, cache.max_seq_len), _arg(mass_dst, "mass_dst", _f32, dev, rows=True),
+        0 if mass_dst is None else _row_stride(mass_dst, seqs, min(evict.budget, cache.max_seq_len)),
         _arg(new_lens, "new_lens", _i32, dev, (seqs,)), _arg(kept, "kept", _i32, dev, (seqs, evict.budget)),
         w, n, _on(stream, dev))
     if status:

@@ -159,6 +159,41 @@ def test_mass_counts_repeats_and_reports_what_is_out_of_range():
     assert (np.abs(g[0] - ref[0]) <= tol[0]).all() and (np.abs(g[1, :64] - ref[1, :64]) <= tol[1, :64]).all()
 
 
+def test_lengths_past_max_seq_len_and_views_too_narrow():
+    """A length above max_seq_len counts as max_seq_len, and a view of a wider
+    tensor that is too narrow for it is refused: nothing outside the view is written."""
+    rng = np.random.default_rng(8)
+    pg = Paged([150, 100], seed=2, max_seq_len=120)
+    call, lat, values = _latents("bf16", rng, pg, 80)
+    q = to_bf16(rng.standard_normal((2, 4, 80)))
+    idx = np.array([[3, 119, 120, 7], [1, 2, 99, -1]], np.int32)  # 120: past max_seq_len
+    good = np.where(idx == 120, -1, idx).astype(np.int32)
+    lse = _true_lse(pg, values, q, good, False, 0.125)
+    cache, dims = pg.cache(), _dims(2, 64, 16, 4, 4, scale=0.125)
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    whole = torch.full((2, 200), -7.0, device="cuda")
+    args = (bf16_cuda(q), *lat, cache, torch.from_numpy(idx).cuda(), torch.from_numpy(lse).cuda(), dims, 1.0)
+    call(*args, None, whole[:, :120], ws)
+    st, info = dsa.workspace_check(ws)
+    assert st == 6 and info >> 24 == 9
+    ref, tol = _reference(pg, values, q, good, lse, 0.0, np.zeros((2, 200), np.float32), False, 0.125, 2)
+    g = whole.double().cpu().numpy()
+    for b, n in enumerate((120, 100)):
+        assert (np.abs(g[b, :n] - ref[b, :n]) <= tol[b, :n]).all() and (g[b, n:] == -7.0).all()
+    with pytest.raises(dsa.DsaError):
+        call(*args, None, whole[:, :119], ws)
+    new_lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    ws = dsa.l4_workspace(dsa.L4_OP_CACHE_EVICT, None, cache)
+    for m, md in ((whole[:, :119], None), (whole[:, :120], torch.zeros(2, 300, device="cuda")[:, :99])):
+        with pytest.raises(dsa.DsaError):
+            dsa.dsa_cache_evict([], cache, dsa.Eviction(100), m, table, md, new_lens, None, ws)
+    wide = torch.full((2, 300), -7.0, device="cuda")
+    dsa.dsa_cache_evict([], cache, dsa.Eviction(100), whole[:, :120], table, wide[:, :100], new_lens, None, ws)
+    assert dsa.workspace_check(ws) == (0, 0) and new_lens.tolist() == [100, 100]
+    assert (wide[:, 100:] == -7.0).all() and (wide[:, :100] != -7.0).all()
+
+
 # ------------------------------------------------------------------ eviction
 def _evict(pg, mass, budget, sinks, recent, pools, rng, ld=None, with_kept=True, max_seq_len=None):
     B = len(pg.lens)
