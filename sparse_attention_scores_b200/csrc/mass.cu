@@ -21,7 +21,9 @@ namespace dsa {
 namespace {
 
 constexpr int kSweep = 256;  // threads of the sweeps over positions
-constexpr double kFixedOne = 1099511627776.0;  // 2^40: a weight of 64 heads x 2^17 rows stays below 2^63
+// 2^40: 65,535 rows, the most a chunk has, of weights below kMostWeight stay below 2^63
+constexpr double kFixedOne = 1099511627776.0;
+constexpr float kMostWeight = 128.f;
 
 struct MassParams {
   const uint16_t *q;
@@ -61,14 +63,16 @@ __global__ void __launch_bounds__(kSweep) decay_kernel(const MassParams p) {
   }
 }
 
-// one row's weight of one kept position
+// One row's weight of one kept position.  With the step's lse it is at most the
+// number of heads; a NaN, and the weights of some other lse, do not go through
+// the fixed point but straight to the result, where a NaN stays one.
 __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos, float w) {
   if (pos < 0 || pos >= p.max_len) return;
-  if (p.rows.causal)
+  if (p.rows.causal && w < kMostWeight)
     atomicAdd(&p.fixed[pos], static_cast<unsigned long long>(
                                  __double2ll_rn(static_cast<double>(w) * kFixedOne)));
   else
-    atomicAdd(&p.mass_out[static_cast<int64_t>(row) * p.mass_ld + pos], w);
+    atomicAdd(&p.mass_out[p.rows.causal ? pos : row * p.mass_ld + pos], w);
 }
 
 

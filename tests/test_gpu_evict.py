@@ -159,6 +159,36 @@ def test_mass_counts_repeats_and_reports_what_is_out_of_range():
     assert (np.abs(g[0] - ref[0]) <= tol[0]).all() and (np.abs(g[1, :64] - ref[1, :64]) <= tol[1, :64]).all()
 
 
+def test_a_nan_in_the_cache_shows_in_the_mass():
+    """A NaN latent row gives NaN masses to the tokens of the rows that kept it
+    (their lse is NaN), in a chunk as in a decode step, and to no others."""
+    rng = np.random.default_rng(12)
+    T, k, H = 70, 8, 16
+    pg = Paged([T], seed=4)
+    call, (pool,), values = _latents("bf16", rng, pg, 80)
+    q = to_bf16(rng.standard_normal((T, H, 80)))
+    idx = select(rng, [t + 1 for t in range(T)], k)
+    bad = [t for t in range(T) if 40 in idx[t]]
+    assert bad
+    lse = _true_lse(pg, values, q, idx, True, 0.125)
+    pool.view(-1, 80)[int(pg.rows(0, [40])[0]), 3] = float("nan")
+    lse[bad] = np.nan
+    cache, dims = pg.cache(), _dims(T, 64, 16, H, k, causal=1, scale=0.125)
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    got = torch.zeros(1, T, device="cuda")
+    call(bf16_cuda(q), pool, cache, torch.from_numpy(idx).cuda(), torch.from_numpy(lse).cuda(), dims, 1.0,
+         None, got, ws)
+    touched = np.zeros(T, bool)
+    for t in bad:
+        touched[idx[t][idx[t] >= 0]] = True
+    assert touched.any() and not touched.all()
+    assert np.array_equal(np.isnan(got[0].cpu().numpy()), touched)
+    g = got[0].double().cpu().numpy()
+    clean = np.where(np.isin(np.arange(T), bad)[:, None], -1, idx).astype(np.int32)
+    ref, tol = _reference(pg, values, q, clean, lse, 0.0, np.zeros((1, T), np.float32), True, 0.125, T)
+    assert (np.abs(g - ref[0])[~touched] <= tol[0][~touched]).all()
+
+
 def test_lengths_past_max_seq_len_and_views_too_narrow():
     """A length above max_seq_len counts as max_seq_len, and a view of a wider
     tensor that is too narrow for it is refused: nothing outside the view is written."""
