@@ -341,6 +341,7 @@ dsa_status_t dsa_cache_evict(const dsa_pool_t *pools, int32_t n_pools, const dsa
   if (!aligned(mass, 4) || !aligned(new_lens, 4) || (mass_dst && !aligned(mass_dst, 4)) ||
       (kept && !aligned(kept, 4)))
     return DSA_ERR_INVALID_ARG;
+  if (mass_dst == mass) return DSA_ERR_INVALID_ARG;  // moved by warps in any order
   if (mass_ld < cache->max_seq_len || (mass_dst && mass_dst_ld < most)) return DSA_ERR_INVALID_ARG;
   EvictLaunch a = {};
   for (int i = 0; i < n_pools; ++i) {

@@ -18,14 +18,14 @@
 // row that puts its largest magnitude in [2^14, 2^15).
 //
 // One CTA per SM takes a contiguous run of 64-key slots of one query row:
-//   warps 0-3    softmax of each slot (warp w: heads 16 w ..),
-//                the rare rescale of O
-//   (both kinds load the query tile first)
+//   warps 0-3       softmax of each slot (warp w: heads 16 w ..), the rare
+//                   rescale of O
 //   warps 4-11, 14  widening: decode a slot from registers, into which the next
-//                slot's bytes are loaded as soon as they are free
-//   warp 13      turns the selected positions into pool rows, ahead of them
-//   warp 12      issues the MMAs: S of a slot as soon as it is
-//                widened, its PV product as soon as its weights are written
+//                   slot's bytes are loaded as soon as they are free
+//   warp 13         turns the selected positions into pool rows, ahead of them
+//   warp 12         issues the MMAs: S of a slot as soon as it is widened, its
+//                   PV product as soon as its weights are written
+// (the first two kinds write the query tile before that).
 // Two slots of the tile ring; S is double-buffered in tensor memory, so S of
 // one slot runs under the softmax of the other, and widening under both
 // products.
@@ -41,7 +41,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kOutWarps = 12;            // warps that read O out, three per tensor memory quadrant
+constexpr int kOutWarps = 12;          // warps that read O out, three per tensor memory quadrant
 constexpr int kTasks = 4;              // widening tasks per warp and slot: 36 over 9 warps
 constexpr int kWeightLog2 = 6;         // weights enter the tensor cores scaled by 2^6
 constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceeded by 2^8
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   uint64_t *sfull = bars + 4;   // [2] S of the slot in tensor memory (MMA commit)
   uint64_t *pready = bars + 6;  // the current slot's weights written (one arrive per softmax warp)
   uint64_t *lofree = bars + 7;  // P lo of the current slot read (MMA commit)
-  uint64_t *qready = bars + 8;  // query tile written (one arrive per softmax warp)
+  uint64_t *qready = bars + 8;  // query tile written (one arrive per warp that wrote some)
   uint64_t *bar_drain = bars + 9;
   uint64_t *bar_stall = bars + 10;
   uint64_t *rowfull = bars + 11;  // [2] the slot's pool rows known (row warp)

@@ -36,6 +36,7 @@ def _cache(num_seqs=2, max_pages=4, num_pages=16, max_seq_len=256, page_size=64,
 
 
 A, WS = ctypes.c_void_p(0x300000), ctypes.c_void_p(0x400000)
+MD = ctypes.c_void_p(0x380000)
 OFF8, OFF2 = ctypes.c_void_p(0x300008), ctypes.c_void_p(0x300002)
 
 
@@ -144,7 +145,7 @@ def test_evict_refuses(L):
     _host_only()
 
     def call(pools=((0x300000, 0x500000, 336),), n=None, c=None, budget=128, sinks=0, recent=0,
-             table=0x600000, mp=2, pages=8, mass=A, ld=256, md=A, mld=128, lens=A, ws=1 << 20):
+             table=0x600000, mp=2, pages=8, mass=A, ld=256, md=MD, mld=128, lens=A, ws=1 << 20):
         arr = (latent4.PoolStruct * max(1, len(pools)))(*[latent4.PoolStruct(*p) for p in pools])
         e = latent4.EvictStruct(budget, sinks, recent, table, mp, pages)
         return L.dsa_cache_evict(arr, len(pools) if n is None else n, c or _cache(), ctypes.byref(e),
@@ -152,7 +153,7 @@ def test_evict_refuses(L):
 
     for bad in (dict(mass=None), dict(lens=None), dict(budget=0), dict(sinks=-1), dict(recent=-1),
                 dict(sinks=100, recent=29), dict(table=None), dict(mp=1), dict(pages=0), dict(ld=255),
-                dict(mld=127), dict(n=5), dict(n=-1), dict(pools=((0, 0x500000, 336),)),
+                dict(mld=127), dict(md=A, mass=A), dict(n=5), dict(n=-1), dict(pools=((0, 0x500000, 336),)),
                 dict(pools=((0x300000, 0x500000, 6),)), dict(pools=((0x300000, 0x500000, 0),)),
                 dict(pools=((0x300008, 0x500000, 336),)), dict(pools=((0x300002, 0x500000, 4),)),
                 dict(c=_cache(num_seqs=0)), dict(mass=OFF2)):
@@ -174,7 +175,7 @@ def test_block_tables_past_32_bit_positions_are_refused(L):
         assert L.dsa_attention_forward_l4(A, A, A, A, A, c, d, A, A, A, WS, 16, None) == st
         assert L.dsa_attention_mass_l4(A, A, c, A, A, d, 1.0, A, A, 256, WS, 16, None) == st
         e = latent4.EvictStruct(128, 0, 0, 0x600000, 2, 8)
-        assert L.dsa_cache_evict(None, 0, c, ctypes.byref(e), A, 256, A, 128, A, None, WS, 16, None) == st
+        assert L.dsa_cache_evict(None, 0, c, ctypes.byref(e), A, 256, MD, 128, A, None, WS, 16, None) == st
 
 
 def test_binding_refuses_what_a_pointer_cannot_carry():
