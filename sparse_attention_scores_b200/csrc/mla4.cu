@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q;
   const uint32_t hi_base = tile + lay.off_p, lo_buf = hi_base + kAtom;  // hi of slot s: + 2 s atoms
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
-  uint64_t *full = bars;        // [2] slot widened (one arrive per widening warp)
+  uint64_t *full = bars;        // [2] slot widened, its keys' powers of two written (widening warps, row warp)
   uint64_t *empty = bars + 2;   // [2] PV of the slot completed (MMA commit)
   uint64_t *sfull = bars + 4;   // [2] S of the slot in tensor memory (MMA commit)
   uint64_t *pready = bars + 6;  // the current slot's weights written (one arrive per softmax warp)
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   while (tmem_cols < static_cast<uint32_t>(2 * kKeys + o_cols)) tmem_cols <<= 1;
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&full[s], kWideWarps);
+      mbar_init(&full[s], kWideWarps + 1);
       mbar_init(&empty[s], 1);
       mbar_init(&sfull[s], 1);
       mbar_init(&rowfull[s], 1);
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   };
   auto task_unit = [&](int i) { return g + kWideWarps * i < 32 ? (lane & 15) : 16 + (lane & 1); };
   uint4 code[kTasks];
-  uint32_t sc[kTasks], eb[kTasks];  // the unit's two block scales, the row's exponent byte
+  uint32_t sc[kTasks];    // the unit's two block scales
   uint32_t have = 0u;               // bit i: task i's row exists
   // The next slot's bytes, into registers.  Every lane loads, from the pool's
   // first row and the row's first unit where it has none of its own (a branch
@@ -232,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       const uint8_t *src = p.latent + static_cast<int64_t>(max(r[i], 0)) * rb;
       code[i] = *reinterpret_cast<const uint4 *>(src + 16 * u);
       sc[i] = ldg_u16(src + W / 2 + 2 * u);
-      eb[i] = ldg_u8(src + W / 2 + nb);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&rowfree[s]);
@@ -414,11 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
           }
           if (tw < words) sts_v4(dst + ((x ^ tw) << 4), h[0], h[1], h[2], h[3]);
         }
-        if (u == 0) {
-          const int e = l4_exponent(eb[i]);
-          keys[s * kKeys + r] = live ? make_float2(pow2i(e), static_cast<float>(e))
-                                     : make_float2(0.f, -INFINITY);
-        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -435,6 +429,24 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       const int place = (h_begin + j) * kKeys + 2 * lane + x;
       return j < nh && place < nsel ? idx[place] : -1;
     };
+    bool live[2] = {false, false};
+    uint32_t eb[2] = {0u, 0u};
+    // the keys' powers of two, a slot behind the rows, so that no slot's rows
+    // wait for them
+    auto publish = [&](int j) -> bool {
+      const int s = j & 1;
+      if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
+      float2 k[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int e = l4_exponent(eb[x]);
+        k[x] = live[x] ? make_float2(pow2i(e), static_cast<float>(e)) : make_float2(0.f, -INFINITY);
+      }
+      *reinterpret_cast<float4 *>(&keys[s * kKeys + 2 * lane]) = make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      return true;
+    };
     int pos[2] = {position(0, 0), position(0, 1)};
     for (int j = 0; j < nh; ++j) {
       const int s = j & 1;
@@ -444,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       for (int x = 0; x < 2; ++x)
         r[x] = l4_pool_row(p.rows, row, pos[x], limit, p.status, kKernMla4,
                            (h_begin + j) * kKeys + 2 * lane + x);
+      if (j > 0 && !publish(j - 1)) break;
       if (j >= 2 && !wait_or_fail(&rowfree[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
       // into L2 ahead of the widening warps' loads: a row is 336 bytes at
       // W = 576, four lines at most
@@ -457,9 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       *reinterpret_cast<int2 *>(&rowi[s * kKeys + 2 * lane]) = make_int2(r[0], r[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&rowfull[s]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        live[x] = r[x] >= 0;
+        eb[x] = ldg_u8(p.latent + static_cast<int64_t>(max(r[x], 0)) * rb + W / 2 + nb);
+      }
       pos[0] = next[0];
       pos[1] = next[1];
     }
+    if (nh > 0 && !*failed) publish(nh - 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
     // The whole warp runs this and branches on votes, so that the descriptors
