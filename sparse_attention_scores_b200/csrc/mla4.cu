@@ -68,24 +68,26 @@ struct Mla4Params {
   DevStatus *status;
 };
 
-// Shared memory: the 2 nmb atoms of slot 0 that PV reads, then three atoms
+// Shared memory: slot 0's nT 64-column atoms (all that PV reads, 2 nmb, and all
+// but one of what S reads, nQ), then three atoms
 // [hi 0 | lo | hi 1], then those of slot 1, the query tile, barriers.  A slot's
-// atom 2 nmb, where it has one (columns that only S reads), lies in its hi
+// atom nT, where it has one (columns that only S reads), lies in its hi
 // atom, which P hi overwrites once S is done with it.  With hi and lo side by
 // side, either slot's weights are one operand of 128 columns (hi | lo, or
 // lo | hi): a wide block of O^T takes both terms in one instruction, at 64
 // cycles against 2 x 48 (measured), and keeps their sums apart until the end.
 struct Layout {
-  int nQ, nmb;        // query atoms, 128-column blocks of the latent rows
+  int nQ, nmb, nT;    // query atoms, 128-column blocks of the latent rows, tile atoms
   uint32_t off_p, off_tile1, off_q, off_misc, bytes;
 };
 __host__ __device__ inline Layout layout_of(int R, int W) {
   Layout l;
   l.nQ = (W + 63) / 64;
   l.nmb = (R + 127) / 128;
-  l.off_p = 2u * l.nmb * kAtom;
+  l.nT = 2 * l.nmb > l.nQ - 1 ? 2 * l.nmb : l.nQ - 1;
+  l.off_p = static_cast<uint32_t>(l.nT) * kAtom;
   l.off_tile1 = l.off_p + 3u * kAtom;
-  l.off_q = l.off_tile1 + 2u * l.nmb * kAtom;
+  l.off_q = l.off_tile1 + static_cast<uint32_t>(l.nT) * kAtom;
   l.off_misc = l.off_q + static_cast<uint32_t>(l.nQ) * kAtom;
   l.bytes = l.off_misc + kMisc;
   return l;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       for (int i = 0; i < kTasks; ++i) {
         const int u = task_unit(i), r = task_row(i), a = u >> 1;
         const bool live = (have >> i) & 1u;
-        const uint32_t dst = r * 128 + (a < 2 * lay.nmb ? tile + a * kAtom + s * lay.off_tile1
+        const uint32_t dst = r * 128 + (a < lay.nT ? tile + a * kAtom + s * lay.off_tile1
                                                         : hi_base + 2 * s * kAtom);
         // the four words in an order turned by the unit, so that eight
         // neighbouring lanes store to eight different 16-byte columns
@@ -491,8 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tile_u = __shfl_sync(0xffffffffu, tile, 0);
     const uint32_t p_u = tile_u + lay.off_p;
     const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;  // of the query; K steps after them
-    const int v_atoms = 2 * lay.nmb;                                // atoms that lie in the tile
-    const int tile_atoms = min(full_atoms, v_atoms);
+    const int tile_atoms = min(full_atoms, lay.nT);
     const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
     bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
     int ns = 0, npv = 0;
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
             mma_f16_elect(d, d_q + ((a * kAtom + k * 32) >> 4), d_p + (k * 32 >> 4), idesc_s, 1u);
         for (int k = 0; k < tail; ++k)
           mma_f16_elect(d, d_q + ((full_atoms * kAtom + k * 32) >> 4),
-                        (full_atoms < v_atoms ? d_l + ((full_atoms * kAtom + k * 32) >> 4)
+                        (full_atoms < lay.nT ? d_l + ((full_atoms * kAtom + k * 32) >> 4)
                                               : d_p + (k * 32 >> 4)),
                         idesc_s, (full_atoms | k) != 0 ? 1u : 0u);
         commit_elect(&sfull[s]);

@@ -65,7 +65,8 @@ def _true_lse(pg, values, q, idx, causal, scale):
 @pytest.mark.parametrize("fmt", ["l4", "l8", "bf16"])
 @pytest.mark.parametrize("B,H,R,P,k,longest", [
     (5, 64, 512, 64, 300, 700), (1, 64, 512, 64, 2048, 5000), (40, 16, 192, 32, 64, 200),
-    (3, 4, 64, 16, 256, 300), (2, 33, 448, 0, 65, 100), (160, 64, 512, 0, 5, 40)])
+    (3, 4, 64, 16, 256, 300), (2, 33, 448, 0, 65, 100), (160, 64, 512, 0, 5, 40),
+    (3, 64, 64, 512, 100, 150)])
 def test_decode_mass(fmt, B, H, R, P, k, longest):
     rng = np.random.default_rng([B, H, R, k])
     lens = rng.integers(1, longest + 1, B).tolist()

@@ -179,6 +179,9 @@ SHAPES = [
     (1, 64, 512, 0, 4097, 6000), (6, 64, 320, 16, 1, 50), (2, 16, 512, 48, 63, 64),
     (1, 64, 512, 64, 20000, 21000), (3, 8, 64, 0, 70, 100), (2, 64, 256, 64, 1024, 2000),
     (40, 64, 384, 32, 200, 400),
+    # more columns that only the logits read than the latent rows' own blocks leave
+    (3, 64, 64, 512, 300, 400), (2, 5, 128, 96, 100, 150), (160, 64, 256, 320, 70, 100),
+    (1, 64, 192, 384, 2048, 2100), (2, 32, 64, 144, 130, 200),
 ]
 
 
