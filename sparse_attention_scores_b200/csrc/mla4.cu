@@ -48,6 +48,7 @@ constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceede
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMisc = 2048;
 constexpr int kMaxSplits = 148;
+constexpr int kMaxAtoms = 9;           // 64-column atoms of a row of 576
 
 struct Mla4Params {
   const uint16_t *q;
@@ -105,6 +106,44 @@ struct Blocks {
     return 2 * kKeys + (mb < wide ? mb * kWideCols : wide * kWideCols + (mb - wide) * kHeads);
   }
 };
+
+// What the MMA warp issues is unrolled: an instruction's operands have to be in
+// uniform registers, and to compute them in loops took longer than some of the
+// instructions run (148 rows of top-2,048 at W = 576: 104.6 us with loops over
+// atoms and blocks, 101.3 with PV unrolled, 93.1 with S too).
+//
+// kAtoms atoms of S, four K steps each
+template <int kAtoms>
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t d_q, uint64_t d_l, uint32_t idesc, uint32_t more) {
+#pragma unroll
+  for (int k = 0; k < 4 * kAtoms; ++k) {
+    const uint32_t at = ((k >> 2) * kAtom + (k & 3) * 32) >> 4;
+    mma_f16_elect(d, d_q + at, d_l + at, idesc, k ? 1u : more);
+  }
+}
+// PV of one slot over kN blocks.  d_v: the CTA's first block in the tile; d_both:
+// [hi | lo] or [lo | hi].
+template <int kN, int kWide>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint64_t d_v, uint64_t d_both, uint64_t d_hi,
+                                         uint64_t d_lo, uint32_t more, uint64_t *lofree) {
+  constexpr uint32_t idesc_wide = idesc_f16_f32(128, kWideCols, 1), idesc_narrow = idesc_f16_f32(128, kHeads, 1);
+#pragma unroll
+  for (int mb = 0; mb < kWide; ++mb)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      mma_f16_elect(o + mb * kWideCols, d_v + ((2 * mb * kAtom + k * 2048) >> 4), d_both + (k * 32 >> 4),
+                    idesc_wide, k ? 1u : more);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int mb = kWide; mb < kN; ++mb)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_f16_elect(o + kWide * kWideCols + (mb - kWide) * kHeads, d_v + ((2 * mb * kAtom + k * 2048) >> 4),
+                      (t ? d_hi : d_lo) + (k * 32 >> 4), idesc_narrow, k | t ? 1u : more);
+    if (t == 0) commit_elect(lofree);
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -488,12 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     // out from one lane.  (From a single-thread branch an instruction took 110
     // cycles to issue, against the 45 to 64 it runs.)
     const uint32_t idesc_s = idesc_f16_f32(kHeads, kKeys, 0);
-    const uint32_t idesc_wide = idesc_f16_f32(128, kWideCols, 1);
-    const uint32_t idesc_pv = idesc_f16_f32(128, kHeads, 1);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tile_u = __shfl_sync(0xffffffffu, tile, 0);
     const uint32_t p_u = tile_u + lay.off_p;
     const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;  // of the query; K steps after them
-    const int tile_atoms = min(full_atoms, lay.nT);
     const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
     bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
     int ns = 0, npv = 0;
@@ -509,23 +545,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         const uint32_t d = tm + kKeys * s;
         const uint64_t d_l = smem_desc(tile_u + s * lay.off_tile1, 16, 1024, kLayoutSW128);
         const uint64_t d_p = smem_desc(p_u + 2 * s * kAtom, 16, 1024, kLayoutSW128);
-        // four K steps per 64-column atom; the columns that only S reads lie
-        // in the P region
-#pragma unroll 4
-        for (int a = 0; a < tile_atoms; ++a)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_elect(d, d_q + ((a * kAtom + k * 32) >> 4), d_l + ((a * kAtom + k * 32) >> 4),
-                          idesc_s, (a | k) != 0 ? 1u : 0u);
-        for (int a = tile_atoms; a < full_atoms; ++a)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_elect(d, d_q + ((a * kAtom + k * 32) >> 4), d_p + (k * 32 >> 4), idesc_s, 1u);
-        for (int k = 0; k < tail; ++k)
-          mma_f16_elect(d, d_q + ((full_atoms * kAtom + k * 32) >> 4),
-                        (full_atoms < lay.nT ? d_l + ((full_atoms * kAtom + k * 32) >> 4)
-                                              : d_p + (k * 32 >> 4)),
-                        idesc_s, (full_atoms | k) != 0 ? 1u : 0u);
+        if (full_atoms == kMaxAtoms) {  // the ninth lies in the hi atom
+          issue_s<kMaxAtoms - 1>(d, d_q, d_l, idesc_s, 0u);
+          issue_s<1>(d, d_q + ((kMaxAtoms - 1) * kAtom >> 4), d_p, idesc_s, 1u);
+        } else {
+          uint64_t q = d_q;
+          for (int a = 0; a < full_atoms; ++a, q += kAtom >> 4)
+            issue_s<1>(d, q, a < lay.nT ? d_l + (a * kAtom >> 4) : d_p, idesc_s, a ? 1u : 0u);
+          const uint64_t l = full_atoms < lay.nT ? d_l + (full_atoms * kAtom >> 4) : d_p;
+          for (int k = 0; k < tail; ++k)
+            mma_f16_elect(d, q + (k * 32 >> 4), l + (k * 32 >> 4), idesc_s, full_atoms | k ? 1u : 0u);
+        }
         commit_elect(&sfull[s]);
         ++ns;
         progressed = true;
@@ -538,28 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         const uint64_t d_both = smem_desc(p_u + s * kAtom, 16, 1024, kLayoutSW128);
         const uint64_t d_hi = smem_desc(p_u + 2 * s * kAtom, 16, 1024, kLayoutSW128);
         const uint64_t d_lo = smem_desc(p_u + kAtom, 16, 1024, kLayoutSW128);
-        const uint32_t o = tm + 2 * kKeys, on = o + ob.wide * kWideCols;  // wide, narrow blocks
-        const uint64_t d_vn = d_v + ((ob.wide * 2 * kAtom) >> 4);
-        const int narrow = ob.n - ob.wide;
-#pragma unroll 2
-        for (int mb = 0; mb < ob.wide; ++mb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_elect(o + mb * kWideCols, d_v + ((2 * mb * kAtom + k * 2048) >> 4),
-                          d_both + (k * 32 >> 4), idesc_wide, k ? 1u : more);
-#pragma unroll 2
-        for (int mb = 0; mb < narrow; ++mb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_elect(on + mb * kHeads, d_vn + ((2 * mb * kAtom + k * 2048) >> 4),
-                          d_lo + (k * 32 >> 4), idesc_pv, k ? 1u : more);
-        commit_elect(lofree);
-#pragma unroll 2
-        for (int mb = 0; mb < narrow; ++mb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_elect(on + mb * kHeads, d_vn + ((2 * mb * kAtom + k * 2048) >> 4),
-                          d_hi + (k * 32 >> 4), idesc_pv, 1u);
+        const uint32_t o = tm + 2 * kKeys;
+        if (ob.n == 4) issue_pv<4, 2>(o, d_v, d_both, d_hi, d_lo, more, lofree);
+        else if (ob.n == 3) issue_pv<3, 3>(o, d_v, d_both, d_hi, d_lo, more, lofree);
+        else if (ob.n == 2) issue_pv<2, 2>(o, d_v, d_both, d_hi, d_lo, more, lofree);
+        else issue_pv<1, 1>(o, d_v, d_both, d_hi, d_lo, more, lofree);
         commit_elect(&empty[s]);
         ++npv;
         progressed = true;
