@@ -115,6 +115,17 @@ constexpr int kTasksOf = (2 * units_of<F>(576) + kWideWarps - 1) / kWideWarps;
 template <int F>
 constexpr int kFillers = F == kLatBf16 ? 4 : kWideWarps;
 
+// The four K steps of atom a.  Unrolled over the atoms of a row of 576: an
+// instruction's operands have to be in uniform registers, and to compute them in
+// a loop took longer than it runs.
+constexpr int kMaxAtoms = 9;
+__device__ __forceinline__ void issue_atom(uint32_t d, int a, uint64_t d_l, uint64_t d_q, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    mma_f16_elect(d + (a & (kParts - 1)) * kHeads, d_l + ((a * kAtom + k * 32) >> 4),
+                  d_q + ((a * kAtom + k * 32) >> 4), idesc, a >= kParts || k != 0 ? 1u : 0u);
+}
+
 template <int F>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -438,12 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       const uint32_t d = tm + s * kParts * kHeads;
       const uint64_t d_l = smem_desc(tile_u + s * lay.slot, 16, 1024, kLayoutSW128);
       // 64-column atom a adds to partial sum a % kParts
-#pragma unroll 4
-      for (int a = 0; a < full_atoms; ++a)
+      if (full_atoms == kMaxAtoms) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16_elect(d + (a & (kParts - 1)) * kHeads, d_l + ((a * kAtom + k * 32) >> 4),
-                        d_q + ((a * kAtom + k * 32) >> 4), idesc, a >= kParts || k != 0 ? 1u : 0u);
+        for (int a = 0; a < kMaxAtoms; ++a) issue_atom(d, a, d_l, d_q, idesc);
+      } else {
+        for (int a = 0; a < full_atoms; ++a) issue_atom(d, a, d_l, d_q, idesc);
+      }
       for (int k = 0; k < tail; ++k)
         mma_f16_elect(d + (full_atoms & (kParts - 1)) * kHeads,
                       d_l + ((full_atoms * kAtom + k * 32) >> 4),
