@@ -12,6 +12,7 @@ by the library raises DsaError.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import sparse_attention_scores_b200 as _dsa
@@ -40,7 +41,12 @@ class EvictStruct(ctypes.Structure):
 
 
 _ready = _torch = _bf16 = _f32 = _i32 = _u8 = None
-_CacheStruct, _DimsStruct, _byref = _dsa.CacheStruct, _dsa.DimsStruct, ctypes.byref
+# dsa_cache_t and dsa_dims_t as packed bytes: half the time of a ctypes structure,
+# which counts in calls whose kernels run a few microseconds
+_pack_cache = struct.Struct("@iPPiiii").pack
+_pack_dims = struct.Struct("@9if").pack
+assert struct.calcsize("@iPPiiii") == ctypes.sizeof(_dsa.CacheStruct)
+assert struct.calcsize("@9if") == ctypes.sizeof(_dsa.DimsStruct)
 
 
 def l4_lib() -> ctypes.CDLL:
@@ -53,7 +59,7 @@ def l4_lib() -> ctypes.CDLL:
         L = _dsa.lib()
         vp, sz, i32, i64, f32 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64,
                                  ctypes.c_float)
-        pc, pd = ctypes.POINTER(_dsa.CacheStruct), ctypes.POINTER(_dsa.DimsStruct)
+        pc = pd = vp  # structures by reference, or their bytes
         pp, pe = ctypes.POINTER(PoolStruct), ctypes.POINTER(EvictStruct)
         end = [vp, sz, vp]  # workspace, its size, stream
         mass_end = [pc, vp, vp, pd, f32, vp, vp, i64] + end
@@ -81,7 +87,7 @@ def l4_lib() -> ctypes.CDLL:
 
 def _device():
     """The current CUDA device's index."""
-    return _torch.cuda.current_device() if not _torch.cuda.is_initialized() else _torch._C._cuda_getDevice()
+    return _torch._C._cuda_getDevice()
 
 
 def _arg(t, name, dtype, device, shape=None, rows=False):
@@ -102,18 +108,21 @@ def _arg(t, name, dtype, device, shape=None, rows=False):
 
 
 def _common(cache, dims, ws, device):
-    """(cache struct, dims struct, workspace pointer, its size) of a call."""
+    """(cache and dims structures, workspace pointer, its size) of a call."""
     lens, table = cache.seq_lens, cache.block_table
     lens_ptr, table_ptr = _arg(lens, "seq_lens", _i32, device), _arg(table, "block_table", _i32, device)
-    seqs, pages = table.shape if table.dim() == 2 else (-1, 0)
-    if lens.shape != (seqs,):
+    shape = table.shape
+    if len(shape) != 2 or lens.shape != shape[:1]:
         raise ValueError("block_table: not [sequences, pages]")
-    return (_byref(_CacheStruct(seqs, lens_ptr, table_ptr, pages, cache.page_size, cache.num_pages,
-                                cache.max_seq_len)),
-            None if dims is None else
-            _byref(_DimsStruct(dims.n_q, dims.H_I, dims.D_I, dims.topk, dims.H, dims.R, dims.P,
-                               dims.causal, dims.q_pos0, dims.scale)),
-            _arg(ws, "ws", _u8, device), ws.numel())
+    try:
+        return (_pack_cache(shape[0], lens_ptr, table_ptr, shape[1], cache.page_size, cache.num_pages,
+                            cache.max_seq_len),
+                None if dims is None else
+                _pack_dims(dims.n_q, dims.H_I, dims.D_I, dims.topk, dims.H, dims.R, dims.P,
+                           dims.causal, dims.q_pos0, dims.scale),
+                _arg(ws, "ws", _u8, device), ws.numel())
+    except struct.error as e:
+        raise ValueError(f"cache or dims: {e}") from None
 
 
 def _on(stream, device):
@@ -331,7 +340,7 @@ def dsa_cache_evict(pools, cache, evict: Eviction, mass, dst_block_table, mass_d
                     _arg(dst_block_table, "dst_block_table", _i32, dev), dst_block_table.shape[1],
                     dst_pages if dst_pages is not None else 1 << 24)
     status = L.dsa_cache_evict(
-        arr, len(pools), c, _byref(e), _arg(mass, "mass", _f32, dev, rows=True),
+        arr, len(pools), c, ctypes.byref(e), _arg(mass, "mass", _f32, dev, rows=True),
         _row_stride(mass, seqs, cache.max_seq_len), _arg(mass_dst, "mass_dst", _f32, dev, rows=True),
         0 if mass_dst is None else _row_stride(mass_dst, seqs, min(evict.budget, cache.max_seq_len)),
         _arg(new_lens, "new_lens", _i32, dev, (seqs,)), _arg(kept, "kept", _i32, dev, (seqs, evict.budget)),
