@@ -82,8 +82,8 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
 // chain add up in the logit: 512 causal rows of 2,048 keys are off by 1.4e-6
 // with one chain of 36, 6.5e-7 with two of 18 (3% slower), 3.4e-7 with four (6%);
 // fp32 additions give 6e-8.
-constexpr int kMisc = 4096;
-constexpr int kFactors = 8;  // ring of the slots' key factors
+constexpr int kMisc = 2048;
+constexpr int kFactors = 4;  // ring of the slots' key factors
 constexpr int kParts = 2;
 struct Layout {
   int nQ;
@@ -147,9 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 14);
   volatile uint32_t *failed = misc + 1;
   float *qmax = reinterpret_cast<float *>(bars + 16);      // [13], padded to 16
-  // [8][64] a key's scale, +inf: unused.  The row warp writes slot j's after the
-  // rows of j - 3 were loaded, so after the tile of j - 4 (bf16: j - 3) was
-  // filled, so after S of j - 6 was formed, after S of j - 8 was read
+  // [4][64] a key's scale, +inf: unused.  The row warp writes slot j's after S of
+  // j - 2 was formed, which is after S of j - 4 was read
   float *factor = qmax + 16;
   int *rowi = reinterpret_cast<int *>(factor + kFactors * kKeys);  // [2][64] pool row, -1: none
 
@@ -386,12 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   } else if (warp == kRowWarp) {
     // --------------------------------------------------------------- pool rows
     // Places 2 lane and 2 lane + 1 of each slot: position, page, pool row, the
-    // key's factor.  The factors are published a slot later, so that no slot's
-    // rows wait for them (read by the filling warps beside the units: 71.1 us
+    // key's factor.  The factors are published a slot later, after the next
+    // slot's rows, so that no rows wait for them (read by the filling warps beside the units: 71.1 us
     // against 66.4 for 148 rows of 2,048 4-bit keys, 86.9 against 78.0 for E4M3).
     bool live[2] = {false, false};
     uint32_t f[2] = {0u, 0u};  // E4M3: the scale; 4-bit: the exponent byte
-    auto publish = [&](int j) {
+    auto publish = [&](int j) -> bool {
+      // `full` of slot j - 2 is complete once its S is, and this arrive is not taken for one of it
+      if (j >= 2 && !wait_or_fail(&sfull[j & 1], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
       float v[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       *reinterpret_cast<float2 *>(&factor[(j & (kFactors - 1)) * kKeys + 2 * lane]) = make_float2(v[0], v[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[j & 1]);
+      return true;
     };
     auto position = [&](int j, int x) -> int {
       const int at = (h_begin + j) * kKeys + 2 * lane + x;
@@ -414,11 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       for (int x = 0; x < 2; ++x)
         r[x] = l4_pool_row(p.rows, row, pos[x], limit, p.status, kKernMass,
                            (h_begin + j) * kKeys + 2 * lane + x);
-      if (j > 0) publish(j - 1);
       if (j >= 2 && !wait_or_fail(&rowfree[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
       *reinterpret_cast<int2 *>(&rowi[s * kKeys + 2 * lane]) = make_int2(r[0], r[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&rowfull[s]);
+      if (j > 0 && !publish(j - 1)) break;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         live[x] = r[x] >= 0;

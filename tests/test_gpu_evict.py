@@ -66,7 +66,7 @@ def _true_lse(pg, values, q, idx, causal, scale):
 @pytest.mark.parametrize("B,H,R,P,k,longest", [
     (5, 64, 512, 64, 300, 700), (1, 64, 512, 64, 2048, 5000), (40, 16, 192, 32, 64, 200),
     (3, 4, 64, 16, 256, 300), (2, 33, 448, 0, 65, 100), (160, 64, 512, 0, 5, 40),
-    (3, 64, 64, 512, 100, 150)])
+    (3, 64, 64, 512, 100, 150), (150, 64, 512, 64, 1000, 1100)])
 def test_decode_mass(fmt, B, H, R, P, k, longest):
     rng = np.random.default_rng([B, H, R, k])
     lens = rng.integers(1, longest + 1, B).tolist()
@@ -112,7 +112,8 @@ def test_decode_mass(fmt, B, H, R, P, k, longest):
 
 @pytest.mark.parametrize("fmt", ["l4", "l8", "bf16"])
 @pytest.mark.parametrize("T,pos0,H,R,P,k", [(100, 0, 64, 512, 64, 64), (33, 500, 16, 192, 32, 300),
-                                            (1, 0, 4, 64, 16, 8), (600, 10, 64, 512, 0, 40)])
+                                            (1, 0, 4, 64, 16, 8), (600, 10, 64, 512, 0, 40),
+                                            (200, 900, 64, 512, 64, 1000)])
 def test_causal_mass_does_not_depend_on_order(fmt, T, pos0, H, R, P, k):
     rng = np.random.default_rng([T, H])
     pg = Paged([pos0 + T], seed=T)
