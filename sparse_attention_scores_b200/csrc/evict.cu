@@ -64,7 +64,8 @@ constexpr int kFlight = 3;
 template <int kRows, typename T>
 __device__ __forceinline__ void copy_rows(const dsa_pool_t &q, int src, int dst, int lane) {
   const int n = q.row_bytes / static_cast<int>(sizeof(T));  // units per row
-  const uint32_t inv = ((1u << 20) + n - 1) / n;            // t / n = t * inv >> 20: t < 4 * 1,024
+  // t / n = t * inv >> 26, exactly: t < 2^13, and inv n exceeds 2^26 by less than n <= 2^10
+  const uint32_t inv = ((1u << 26) + n - 1) / n;
   const T *s = static_cast<const T *>(q.src);
   T *d = static_cast<T *>(q.dst);
   for (int t0 = 0; t0 < kRows * n; t0 += 32 * kFlight) {
@@ -73,7 +74,7 @@ __device__ __forceinline__ void copy_rows(const dsa_pool_t &q, int src, int dst,
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
       const int t = t0 + 32 * u + lane;
-      const int r = min(static_cast<int>((static_cast<uint64_t>(t) * inv) >> 20), kRows - 1);
+      const int r = min(static_cast<int>((static_cast<uint64_t>(t) * inv) >> 26), kRows - 1);
       const int c = t - r * n;
       const int from = __shfl_sync(0xffffffffu, src, r), to = __shfl_sync(0xffffffffu, dst, r);
       at[u] = t < kRows * n && from >= 0 ? static_cast<int64_t>(to) * n + c : -1;

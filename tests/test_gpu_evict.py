@@ -296,6 +296,26 @@ def test_evict_keeps_and_moves_exactly(kind, lens, budget, sinks, recent):
     assert torch.equal(again[3], new_lens)
 
 
+@pytest.mark.parametrize("widths", [(4, 4092, 4096, 2128), (1, 1023, 532, 6), (84,), ()])
+def test_evict_moves_rows_of_any_width(widths):
+    """Row widths (in 4-byte units) from the smallest to the largest, odd ones among them."""
+    rng = np.random.default_rng(len(widths))
+    for lens, budget in (([300, 90], 128), ([9000] * 5, 4000)):
+        pg = Paged(lens, seed=6)
+        mass = rng.exponential(1.0, (len(lens), max(lens))).astype(np.float32)
+        pools = [torch.randint(-2 ** 31, 2 ** 31 - 1, (pg.num_pages, 64, min(w, 1024)), dtype=torch.int32,
+                               device="cuda") for w in widths]
+        dst, table, _, new_lens, kept, st = _evict(pg, mass, budget, 2, 30, pools, rng)
+        assert st == (0, 0)
+        for b, n in enumerate(lens):
+            keep = l4.evict_keep(mass[b, :n], budget, 2, 30)
+            i = np.arange(len(keep))
+            to = torch.from_numpy(table[b][i // 64].astype(np.int64) * 64 + i % 64).cuda()
+            src = torch.from_numpy(pg.rows(b, keep)).cuda()
+            for p, d in zip(pools, dst):
+                assert torch.equal(d.flatten(0, 1)[to], p.flatten(0, 1)[src])
+
+
 def test_evict_reports_pages_out_of_range():
     rng = np.random.default_rng(2)
     pg = Paged([200, 200], seed=3)
