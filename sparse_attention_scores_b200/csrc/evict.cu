@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const EvictParams p) 
     const int i = i0 + lane;
     int src = -1, dst = -1;
     if (lane < kRows && i < n) {
-      const int pos = p.kept[b * p.kept_ld + i];
+      // a selection that timed out (and was reported) may have left anything here
+      const int pos = min(max(p.kept[b * p.kept_ld + i], 0), p.lens[b] - 1);
       const int sp = p.src_table[static_cast<int64_t>(b) * p.src_max_pages + pos / kPageSize];
       const int dp = p.dst_table[static_cast<int64_t>(b) * p.dst_max_pages + i / kPageSize];
       if (p.mass_dst) p.mass_dst[b * p.mass_dst_ld + i] = p.mass[b * p.mass_ld + pos];
