@@ -130,7 +130,8 @@ DSA_API dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float
  *             written (len(b): seq_lens[b], at most max_seq_len; for a causal
  *             chunk q_pos0 + n_q); entries past that are left untouched, and
  *             so is everything when n_q = 0.  mass_ld >= max_seq_len, for a
- *             causal chunk >= q_pos0 + n_q
+ *             causal chunk >= q_pos0 + n_q (which is sequence 0: only row 0
+ *             is written)
  * A position that a row holds twice counts twice.  Causal chunks add their
  * rows in 64-bit fixed point (steps of 2^-40), so the result does not depend
  * on the order in which the rows ran (a NaN weight, and one of 128 or more, which

@@ -214,7 +214,7 @@ struct QueryPieces {
 #pragma unroll
     for (int i = 0; i < kSoftWarps + kWideWarps; ++i) mx = fmaxf(mx, qmax[i]);
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-    return mx == 0.f ? 0 : max(-100, min(100, 14 - ex));
+    return mx == 0.f ? 0 : min(126, 14 - ex);  // ex <= 127: at least -113
   }
 
   // kScaled: as fp16, times 2^k; else as it is (bf16).  Each worker warp

@@ -222,6 +222,20 @@ def test_prefill_matches_definition(T, pos0, H, R, P, k):
     _check_attention(q, values, pg, idx, out, lse, R, 0.0625, True)
 
 
+@pytest.mark.parametrize("power", [115, -110])
+def test_queries_of_any_size_carry_over(power):
+    """q times a power of two and scale divided by it: the same products, bit for
+    bit, up to the ends of bf16."""
+    rng = np.random.default_rng(3)
+    pg = Paged([300, 200], seed=3)
+    pool, _ = random_l4(rng, pg.num_pages, 576)
+    q, idx = to_bf16(rng.standard_normal((2, 64, 576))), select(rng, [300, 200], 130)
+    runs = [_run_mla(pg, pool, q * 2.0 ** p, idx, _dims(2, 576, 64, topk=130, H=64, scale=0.0625 * 2.0 ** -p))
+            for p in (0, power)]
+    assert runs[0][2] == runs[1][2] == (0, 0)
+    assert np.array_equal(runs[0][0], runs[1][0]) and np.array_equal(runs[0][1], runs[1][1])
+
+
 def test_logits_far_apart_and_rows_of_unequal_size():
     """Weights from 1 to 0, token exponents far apart, heads of tiny and large
     queries in one row, a token of zeros."""
