@@ -110,7 +110,7 @@ constexpr int kTasksOf = (2 * units_of<F>(576) + kWideWarps - 1) / kWideWarps;
 // warps fill the even slots and four the odd ones, so that a slot is announced
 // when its own copies have landed (with one group for both, one slot's copies
 // were issued between another's arrival and its announcement: 349 us against
-// 266 for 512 causal rows of 2,048 keys).  What is left is the copies' own rate,
+// 266 for 512 causal rows of 2,048 keys; 231 since S's issue is unrolled).  What is left is the copies' own rate,
 // about 17 bytes a cycle and SM.
 template <int F>
 constexpr int kFillers = F == kLatBf16 ? 4 : kWideWarps;
@@ -386,8 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     // --------------------------------------------------------------- pool rows
     // Places 2 lane and 2 lane + 1 of each slot: position, page, pool row, the
     // key's factor.  The factors are published a slot later, after the next
-    // slot's rows, so that no rows wait for them (read by the filling warps beside the units: 71.1 us
-    // against 66.4 for 148 rows of 2,048 4-bit keys, 86.9 against 78.0 for E4M3).
+    // slot's rows, so that no rows wait for them (read
+    // by the filling warps beside the units: 75.3 us against 68.8 for 148 rows of
+    // 2,048 4-bit keys, 90.2 against 82.8 for E4M3).
     bool live[2] = {false, false};
     uint32_t f[2] = {0u, 0u};  // E4M3: the scale; 4-bit: the exponent byte
     auto publish = [&](int j) -> bool {

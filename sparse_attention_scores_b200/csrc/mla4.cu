@@ -826,7 +826,7 @@ dsa_status_t launch_mla4(const Mla4Launch &a, cudaStream_t stream) {
   p.status = a.status;
   // While CTAs still leave SMs idle, a split's output columns go to 2 or 4 of
   // them: each forms the logits anew, but multiplies and stores its share only
-  // (one row of top-2,048: 15.8 us with one CTA a split, 13.6 with four).
+  // (one row of top-2,048: 15.1 us with one CTA a split, 13.0 with four).
   const int nmb = (a.R + 127) / 128;
   p.ncb = 1;
   for (int c = 2; c <= 4; c *= 2)
