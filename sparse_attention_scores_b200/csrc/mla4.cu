@@ -30,6 +30,11 @@
 // one slot runs under the softmax of the other, and widening under both
 // products.
 //
+// What bounds it: a slot's chain of widening, S, softmax and PV with two slots in
+// flight, 8,700 cycles for two at W = 576 (148 rows of top-2,048: 89 us), of which
+// the MMAs' issue is busy for 5,900.  Operands, tiles and weights are 400 KB of
+// shared-memory traffic per slot, 6,200 cycles for two at 128 bytes a cycle.
+//
 // A row split over several CTAs leaves (m, l, O) partials in global scratch
 // (they stay in L2) and a merge kernel combines them.
 #include <math.h>
@@ -109,8 +114,8 @@ struct Blocks {
 
 // What the MMA warp issues is unrolled: an instruction's operands have to be in
 // uniform registers, and to compute them in loops took longer than some of the
-// instructions run (148 rows of top-2,048 at W = 576: 104.6 us with loops over
-// atoms and blocks, 101.3 with PV unrolled, 93.1 with S too).
+// instructions run (148 rows of top-2,048 at W = 576: 98.3 us with loops over
+// atoms and blocks, 89.0 unrolled; one row 13.3 against 12.9).
 //
 // kAtoms atoms of S, four K steps each
 template <int kAtoms>
