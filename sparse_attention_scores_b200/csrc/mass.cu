@@ -83,7 +83,6 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
 // with one chain of 36, 6.5e-7 with two of 18 (3% slower), 3.4e-7 with four (6%);
 // fp32 additions give 6e-8.
 constexpr int kMisc = 2048;
-constexpr int kFactors = 4;  // ring of the slots' key factors
 constexpr int kParts = 2;
 struct Layout {
   int nQ;
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   const uint32_t tile = smem_u32(smem), qs = tile + lay.off_q;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.off_misc);
   uint64_t *full = bars;         // [2] slot filled, its key factors written (filling warps, row warp)
-  uint64_t *sread = bars + 2;    // [2] S read (one arrive per summing warp)
+  uint64_t *sread = bars + 2;    // [2] S and key factors read (one arrive per summing warp)
   uint64_t *sfull = bars + 4;    // [2] S in tensor memory, the slot's tile free (MMA commit)
   uint64_t *rowfull = bars + 6;  // [2] the slot's pool rows known (row warp)
   uint64_t *rowfree = bars + 8;  // [2] and read (one arrive per filling warp)
@@ -147,10 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 14);
   volatile uint32_t *failed = misc + 1;
   float *qmax = reinterpret_cast<float *>(bars + 16);      // [13], padded to 16
-  // [4][64] a key's scale, +inf: unused.  The row warp writes slot j's after S of
-  // j - 2 was formed, which is after S of j - 4 was read
+  // [2][64] a key's scale, +inf: unused
   float *factor = qmax + 16;
-  int *rowi = reinterpret_cast<int *>(factor + kFactors * kKeys);  // [2][64] pool row, -1: none
+  int *rowi = reinterpret_cast<int *>(factor + 2 * kKeys);  // [2][64] pool row, -1: none
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int split = blockIdx.x;
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       tc_fence_after();
       uint32_t v[32];
       tmem_ld_16x256b_x8(tmem + lane_off + s * kParts * kHeads, v);
-      const float *f = factor + (j & (kFactors - 1)) * kKeys + k0;
+      const float *f = factor + s * kKeys + k0;
       const float f0 = f[0], f1 = f[8];
       tmem_ld_wait();
       for (int x = 1; x < min(kParts, lay.nQ); ++x) {
@@ -392,14 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     bool live[2] = {false, false};
     uint32_t f[2] = {0u, 0u};  // E4M3: the scale; 4-bit: the exponent byte
     auto publish = [&](int j) -> bool {
-      // `full` of slot j - 2 is complete once its S is, and this arrive is not taken for one of it
-      if (j >= 2 && !wait_or_fail(&sfull[j & 1], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
+      // after slot j - 2 was read: its factors are free, and `full` cannot pass
+      // through this slot's phase while a summing warp has yet to see that one's
+      if (j >= 2 && !wait_or_fail(&sread[j & 1], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
       float v[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         v[x] = !live[x] ? INFINITY
                         : (F == kLatBf16 ? 1.f : (F == kLatE4m3 ? __uint_as_float(f[x]) : pow2i(l4_exponent(f[x]))));
-      *reinterpret_cast<float2 *>(&factor[(j & (kFactors - 1)) * kKeys + 2 * lane]) = make_float2(v[0], v[1]);
+      *reinterpret_cast<float2 *>(&factor[(j & 1) * kKeys + 2 * lane]) = make_float2(v[0], v[1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[j & 1]);
       return true;

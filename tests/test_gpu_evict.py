@@ -140,6 +140,27 @@ def test_causal_mass_does_not_depend_on_order(fmt, T, pos0, H, R, P, k):
     assert (g[0, n:] == -7.0).all()
 
 
+@pytest.mark.parametrize("fmt", ["l4", "l8", "bf16"])
+@pytest.mark.parametrize("T,pos0,H,R,P,k", [(200, 800, 4, 256, 64, 1000), (300, 2000, 64, 64, 16, 2048)])
+def test_mass_of_long_rows_repeats_bit_for_bit(fmt, T, pos0, H, R, P, k):
+    """Rows of many slots, narrow or with few heads, so that the filling, the
+    products and the sums run at different paces: no wait gives up, and every
+    run adds the same weights."""
+    rng = np.random.default_rng([T, k])
+    pg = Paged([pos0 + T], seed=T)
+    call, lat, values = _latents(fmt, rng, pg, R + P)
+    q = bf16_cuda(to_bf16(0.3 * rng.standard_normal((T, H, R + P))))
+    idx = torch.from_numpy(select(rng, [pos0 + t + 1 for t in range(T)], k)).cuda()
+    lse = torch.full((T, H), 8.0, device="cuda")
+    cache, dims = pg.cache(), _dims(T, R, P, H, k, causal=1, q_pos0=pos0)
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    runs = [torch.zeros(1, pos0 + T, device="cuda") for _ in range(40)]
+    for got in runs:
+        call(q, *lat, cache, idx, lse, dims, 1.0, None, got, ws)
+    assert dsa.workspace_check(ws) == (0, 0)
+    assert all(torch.equal(runs[0], got) for got in runs) and float(runs[0].sum()) > 0
+
+
 def test_mass_counts_repeats_and_reports_what_is_out_of_range():
     rng = np.random.default_rng(5)
     pg = Paged([100, 64], seed=1)
