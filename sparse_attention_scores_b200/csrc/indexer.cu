@@ -248,7 +248,10 @@ __global__ void __launch_bounds__(threads_of<NEG, K8>(), NEG == 1 ? 2 : 1)
   constexpr bool kMayDyn = NEG == 2 || !K8;
   const bool dyn = kMayDyn && p.static_pct < 100 && nqb == 2 &&
                    total >= kMinDynUnits * static_cast<int>(gridDim.x);
-  const int st_total = static_cast<int>((static_cast<int64_t>(total) * min(p.static_pct, 100)) / 100);
+  // without the counter all of them, also where the host (which knows only the
+  // longest row) had made room for it
+  const int st_total =
+      dyn ? static_cast<int>((static_cast<int64_t>(total) * min(p.static_pct, 100)) / 100) : total;
   const int s0 = static_cast<int>((static_cast<int64_t>(st_total) * blockIdx.x) / gridDim.x);
   const int s1 = static_cast<int>((static_cast<int64_t>(st_total) * (blockIdx.x + 1)) / gridDim.x);
   // counter chunks: about two per CTA of what the static share leaves,
