@@ -11,11 +11,18 @@
 //   O^T += L^T . P^T   M = 128 latent columns per block, N = 64 heads, K = 64 keys
 // The row's 2^e stays out of the tiles.  In base-2 units, with z2 = z log2(e):
 //   w[h, j] = 2^(z2 + e_j - m_h),  m_h a running maximum of z2 + e_j,
-//   out = sum w s v / sum w 2^-e_j,   lse = (m + log2 sum w 2^-e_j) ln 2
-// so weights stay in (0, 1] whatever the tokens' sizes (|e| <= 60 keeps every
-// factor inside fp32), and enter the second product as two fp16 terms, hi + lo
-// (22 bits), scaled by 2^6.  q enters as fp16 after one power of two per query
-// row that puts its largest magnitude in [2^14, 2^15).
+//   out = sum w s v / l,   lse = (m + log2 l) ln 2,   l = sum 2^(z2 - m)
+// so weights stay in (0, 1] whatever the tokens' sizes, and enter the second
+// product as two fp16 terms, hi + lo (22 bits), scaled by 2^6: an element of out
+// loses what is below 2^-31 of the row's largest product w s v.  q enters as fp16
+// after one power of two per query row that puts its largest magnitude in
+// [2^14, 2^15).
+//   l is summed as w 2^-e_j while every token has |e| <= 24 (rows whose largest
+// magnitude is between 8e-5 and 4.5e10): a w that fp32 flushes, below 2^-126, is
+// then below 2^-78 of l.  With larger |e| it need not be: 2^-120 lies between e =
+// -60 and e = 60.  From the first such slot on, l is summed from z2 itself against
+// a running maximum of z2 and brought back to m's units at the end; the merge of
+// the splits does likewise.
 //
 // One CTA per SM takes a contiguous run of 64-key slots of one query row:
 //   warps 0-3       softmax of each slot (warp w: heads 16 w ..), the rare
@@ -40,6 +47,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "l4_tile.cuh"
 
@@ -52,6 +60,7 @@ constexpr int kWeightLog2 = 6;         // weights enter the tensor cores scaled 
 constexpr float kRescaleLog2 = 8.f;    // the running maximum moves when exceeded by 2^8
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kMisc = 2048;
+constexpr int kFarExp = 24;            // rows that hold a token with a larger |e| have l summed from z2
 constexpr int kMaxSplits = 148;
 constexpr int kMaxAtoms = 9;           // 64-column atoms of a row of 576
 
@@ -150,6 +159,28 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint64_t d_v, uint64_t d_bo
   }
 }
 
+// z2 of two keys, k = their (2^e, e), under the thread's two heads: 8 columns of
+// S; -inf where a key is unused
+__device__ __forceinline__ void load_z(uint32_t taddr, const float4 &k, float zscale, float (&z)[4]) {
+  uint32_t v[4];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr));
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float scale = i & 1 ? k.z : k.x;  // 0: unused
+    z[i] = scale == 0.f ? -INFINITY : __uint_as_float(v[i]) * (scale * zscale);
+  }
+}
+// moves a running maximum that a slot exceeds by 2^8; what its sums are multiplied by
+__device__ __forceinline__ float raise(float &m, float x) {
+  if (!(x > m + kRescaleLog2 || m == -INFINITY)) return 1.f;
+  const float a = x == m ? 1.f : ex2(m - x);
+  m = x;
+  return a;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -176,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
   float *alpha = qmax + 16;                             // [64]
   float2 *keys = reinterpret_cast<float2 *>(alpha + kHeads);    // [2][64] (2^e, e); (0, -inf): unused
   int *rowi = reinterpret_cast<int *>(keys + 2 * kKeys);        // [2][64] pool row, -1: none
+  // [2] a key of this slot, or of one in its place before, has |e| > kFarExp
+  volatile uint32_t *far = reinterpret_cast<uint32_t *>(rowi + 2 * kKeys);
   float *mfin = reinterpret_cast<float *>(keys);                // [64], [64]: after the loop
   float *lfin = mfin + kHeads;
 
@@ -204,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     mbar_init(bar_drain, 1);
     mbar_init(bar_stall, 1);
     *failed = 0u;
+    far[0] = far[1] = 0u;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -306,12 +340,39 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     const uint32_t prow0 = h0 * 128, prow1 = h1 * 128, pcol = c2 * 2;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool alive = true;
-    for (int j = 0; j < nh; ++j) {
+    // O times what the sums of the slots before slot j > 0 are multiplied by
+    auto rescale = [&](int j, float a0, float a1) {
+      // O holds every earlier slot once PV(j - 1) has completed
+      if ((lane & 3) == 0) {
+        alpha[h0] = a0;
+        alpha[h1] = a1;
+      }
+      alive = wait_or_fail(&empty[(j - 1) & 1], ((j - 1) >> 1) & 1, p.wait_ns, failed);
+      bar_sync(1, 32 * kSoftWarps);
+      tc_fence_after();
+      if (alive)
+        for (int u = 0; u < o_cols / 32; ++u) {
+          const uint32_t ta = tmem + lane_off + 2 * kKeys + 32 * u;
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(ta, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[32 * (u & 1) + i]);
+          tmem_st_32x32b_x32(ta, o);
+        }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      bar_sync(1, 32 * kSoftWarps);  // alpha may be rewritten
+    };
+    int j = 0;
+    bool from_z = false;
+    for (; j < nh; ++j) {
       const int s = j & 1;
       const uint32_t par = (j >> 1) & 1;
       alive = alive && wait_or_fail(&sfull[s], par, p.wait_ns, failed) &&
               wait_or_fail(&full[s], par, p.wait_ns, failed);
       tc_fence_after();
+      from_z = far[s];  // the same for all four warps
       // z2 + e of this thread's 16 keys of two heads
       uint32_t v[32];
       tmem_ld_16x256b_x8(tmem + lane_off + kKeys * s, v);
@@ -346,30 +407,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         a1 = x1 == m1 ? 1.f : ex2(m1 - x1);
         m1 = x1;
       }
-      const bool need = j > 0 && ((a0 != 1.f && h0 < p.H) || (a1 != 1.f && h1 < p.H));
+      const bool need = from_z || (j > 0 && ((a0 != 1.f && h0 < p.H) || (a1 != 1.f && h1 < p.H)));
       if (bar_or(1, 32 * kSoftWarps, need || !alive)) {
-        // O holds every earlier slot once PV(j - 1) has completed
+        from_z = from_z && alive;
         if (bar_or(1, 32 * kSoftWarps, !alive)) break;
-        if ((lane & 3) == 0) {
-          alpha[h0] = a0;
-          alpha[h1] = a1;
+        if (j > 0) rescale(j, a0, a1);
+        if (from_z) {
+          l0 *= a0;
+          l1 *= a1;
+          break;
         }
-        alive = wait_or_fail(&empty[(j - 1) & 1], ((j - 1) >> 1) & 1, p.wait_ns, failed);
-        bar_sync(1, 32 * kSoftWarps);
-        tc_fence_after();
-        if (alive)
-          for (int u = 0; u < o_cols / 32; ++u) {
-            const uint32_t ta = tmem + lane_off + 2 * kKeys + 32 * u;
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(ta, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[32 * (u & 1) + i]);
-            tmem_st_32x32b_x32(ta, o);
-          }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        bar_sync(1, 32 * kSoftWarps);  // alpha may be rewritten
       }
       // weights, 2^6 of them, and their share of l
       const float f0 = (m0 == -INFINITY ? 0.f : m0) - kWeightLog2;
@@ -409,6 +456,80 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && alive) mbar_arrive(pready);
+    }
+    // The same from the first slot with a far key on, l apart from the weights (a
+    // second exponential per key).  A rolled loop of its own, from S in tensor
+    // memory: inside the loop above, or unrolled beside it, it took registers from
+    // every row (2,300 causal rows 883 and 845 us, 823 so, 813 without it).
+    if (j < nh && from_z) {
+      float n0 = m0, n1 = m1;  // what l is relative to
+      for (; j < nh; ++j) {
+        const int s = j & 1;
+        const uint32_t par = (j >> 1) & 1;
+        alive = alive && wait_or_fail(&sfull[s], par, p.wait_ns, failed) &&
+                wait_or_fail(&full[s], par, p.wait_ns, failed);
+        tc_fence_after();
+        const uint32_t ta = tmem + lane_off + kKeys * s;
+        const float2 *key = keys + s * kKeys + c2;
+        float x0 = -INFINITY, x1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const float4 k = *reinterpret_cast<const float4 *>(key + 8 * i);
+          float z[4];
+          load_z(ta + 8 * i, k, zscale, z);
+          x0 = fmaxf(x0, fmaxf(z[0] + k.y, z[1] + k.w));
+          x1 = fmaxf(x1, fmaxf(z[2] + k.y, z[3] + k.w));
+          y0 = fmaxf(y0, fmaxf(z[0], z[1]));
+          y1 = fmaxf(y1, fmaxf(z[2], z[3]));
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+          y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
+          y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
+        }
+        const float a0 = raise(m0, x0), a1 = raise(m1, x1);
+        l0 *= raise(n0, y0);
+        l1 *= raise(n1, y1);
+        const bool need = j > 0 && ((a0 != 1.f && h0 < p.H) || (a1 != 1.f && h1 < p.H));
+        if (bar_or(1, 32 * kSoftWarps, need || !alive)) {
+          if (bar_or(1, 32 * kSoftWarps, !alive)) break;
+          rescale(j, a0, a1);
+        }
+        if (j > 0) alive = wait_or_fail(lofree, (j - 1) & 1, p.wait_ns, failed) && alive;
+        const float f0 = (m0 == -INFINITY ? 0.f : m0) - kWeightLog2;
+        const float f1 = (m1 == -INFINITY ? 0.f : m1) - kWeightLog2;
+        const float g0 = (n0 == -INFINITY ? 0.f : n0) - kWeightLog2;
+        const float g1 = (n1 == -INFINITY ? 0.f : n1) - kWeightLog2;
+        const uint32_t hb = hi_base + 2 * s * kAtom;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const float4 k = *reinterpret_cast<const float4 *>(key + 8 * i);
+          float z[4];
+          load_z(ta + 8 * i, k, zscale, z);
+          l0 += ex2(z[0] - g0) + ex2(z[1] - g0);
+          l1 += ex2(z[2] - g1) + ex2(z[3] - g1);
+          const float wa0 = ex2(z[0] + k.y - f0), wb0 = ex2(z[1] + k.w - f0);
+          const float wa1 = ex2(z[2] + k.y - f1), wb1 = ex2(z[3] + k.w - f1);
+          const uint32_t hi0 = pack_f16(wa0, wb0), hi1 = pack_f16(wa1, wb1);
+          const float2 t0 = __half22float2(as_half2(hi0)), t1 = __half22float2(as_half2(hi1));
+          const uint32_t ch = static_cast<uint32_t>((i ^ r0) << 4) + pcol;
+          if (alive) {
+            sts_u32(hb + prow0 + ch, hi0);
+            sts_u32(hb + prow1 + ch, hi1);
+            sts_u32(lo_buf + prow0 + ch, pack_f16(wa0 - t0.x, wb0 - t0.y));
+            sts_u32(lo_buf + prow1 + ch, pack_f16(wa1 - t1.x, wb1 - t1.y));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && alive) mbar_arrive(pready);
+      }
+      // into m's units: |e| <= 60 keeps n - m within 100, and l inside fp32
+      l0 = l0 != 0.f ? l0 * ex2(n0 - m0) : 0.f;
+      l1 = l1 != 0.f ? l1 * ex2(n1 - m1) : 0.f;
     }
     // the last PV has to complete before O and the lo buffer are used
     if (nh > 0) wait_or_fail(&empty[(nh - 1) & 1], ((nh - 1) >> 1) & 1, p.wait_ns, failed);
@@ -478,17 +599,20 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     bool live[2] = {false, false};
     uint32_t eb[2] = {0u, 0u};
     // the keys' powers of two, a slot behind the rows, so that no slot's rows
-    // wait for them
+    // wait for them, and whether one is far
     auto publish = [&](int j) -> bool {
       const int s = j & 1;
-      if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
       float2 k[2];
+      bool wide = false;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int e = l4_exponent(eb[x]);
+        wide |= live[x] && eb[x] - (127u - kFarExp) > 2u * kFarExp;
         k[x] = live[x] ? make_float2(pow2i(e), static_cast<float>(e)) : make_float2(0.f, -INFINITY);
       }
+      if (j >= 2 && !wait_or_fail(&empty[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) return false;
       *reinterpret_cast<float4 *>(&keys[s * kKeys + 2 * lane]) = make_float4(k[0].x, k[0].y, k[1].x, k[1].y);
+      if (wide) far[s] = 1u;
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[s]);
       return true;
@@ -676,7 +800,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
 }
 
 // Combine the split partials of one (row, head):
-//   out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s,  lse = (M + log2 L) ln 2
+//   out = sum_s 2^(m_s - M) O_s / (2^D L),  lse = (M + D + log2 L) ln 2,
+//   L = sum_s 2^(m_s - M - D) l_s
+// D is 0 while no m_s is below M - 60 (l_s is between 2^-54 and 2^97), else an
+// integer near log2 of the largest 2^(m_s - M) l_s: what a split with a small m
+// holds of l may be most of it (l counts tokens by their weight, m by their weight
+// times their size), however far 2^(m_s - M) lies below fp32.
 // One CTA per (row, head): kGroups groups of 128 threads take every kGroups-th
 // split, a thread four columns.  The loads of O (kMergeBatch splits per group
 // at once) are in flight while one warp forms the splits' weights, so the
@@ -688,7 +817,7 @@ constexpr int kMergeBatch = 8;
 template <int kGroups>
 __global__ void __launch_bounds__(128 * kGroups) mla4_merge_kernel(const Mla4Params p) {
   __shared__ float wt[kMaxSplits];
-  __shared__ float tot[2];
+  __shared__ float tot[3];
   __shared__ float4 part[kGroups][128];
   griddep_wait();
   griddep_launch_dependents();
@@ -708,22 +837,42 @@ __global__ void __launch_bounds__(128 * kGroups) mla4_merge_kernel(const Mla4Par
   load(grp);
   const float *ml = p.part_ml + static_cast<int64_t>(row) * p.nsplit * 2 * p.H;
   if (tid < 32) {
-    float M = -INFINITY;
+    float M = -INFINITY, D = 0.f, L = 0.f;
     for (int s = lane; s < p.nsplit; s += 32) M = fmaxf(M, ml[s * 2 * p.H + h]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
+    bool far = false;
     for (int s = lane; s < p.nsplit; s += 32) {
       const float m = ml[s * 2 * p.H + h], l = ml[s * 2 * p.H + p.H + h];
       const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+      far |= m != -INFINITY && m - M < -60.f;
       wt[s] = w;
       L += w == 0.f ? 0.f : w * l;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+      D = -126.f;
+      L = 0.f;
+#pragma unroll 1
+      for (int s = lane; s < p.nsplit; s += 32) {
+        const float m = ml[s * 2 * p.H + h], l = ml[s * 2 * p.H + p.H + h];  // l > 0 where m is finite
+        const int k = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+        if (m != -INFINITY) D = fmaxf(D, ceilf(m - M) + static_cast<float>(k));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) D = fmaxf(D, __shfl_xor_sync(0xffffffffu, D, o));
+      D = fminf(D, 126.f);
+#pragma unroll 1
+      for (int s = lane; s < p.nsplit; s += 32) {
+        const float m = ml[s * 2 * p.H + h], l = ml[s * 2 * p.H + p.H + h];
+        L += m == -INFINITY ? 0.f : exp2f(m - M - D) * l;
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) {
       tot[0] = M;
       tot[1] = L;
+      tot[2] = D;
     }
   }
   __syncthreads();
@@ -756,7 +905,8 @@ __global__ void __launch_bounds__(128 * kGroups) mla4_merge_kernel(const Mla4Par
       }
     }
   }
-  const float L = tot[1], il = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+  const float L = tot[1], D = tot[2];
+  const float il = L > 0.f ? pow2i(-static_cast<int>(D)) / L : (L == L ? 0.f : L);
   if (grp == 0 && c < p.R) {
     float *out = p.out + (static_cast<int64_t>(row) * p.H + h) * p.R + c;  // 4-byte aligned only
     out[0] = acc.x * il;
@@ -766,7 +916,7 @@ __global__ void __launch_bounds__(128 * kGroups) mla4_merge_kernel(const Mla4Par
   }
   if (tid == 0)
     p.lse[static_cast<int64_t>(row) * p.H + h] =
-        L > 0.f ? (tot[0] + log2f(L)) * kLn2 : (L == L ? -INFINITY : L);
+        L > 0.f ? (tot[0] + (D + log2f(L))) * kLn2 : (L == L ? -INFINITY : L);
 }
 
 // Splits of a row: while rows leave SMs idle, as many CTAs per row as fit one
