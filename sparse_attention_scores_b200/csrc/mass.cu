@@ -146,9 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(bars + 14);
   volatile uint32_t *failed = misc + 1;
   float *qmax = reinterpret_cast<float *>(bars + 16);      // [13], padded to 16
-  // [2][64] a key's scale, +inf: unused
-  float *factor = qmax + 16;
+  float *factor = qmax + 16;                                // [2][64] a key's scale
   int *rowi = reinterpret_cast<int *>(factor + 2 * kKeys);  // [2][64] pool row, -1: none
+  uint2 *used = reinterpret_cast<uint2 *>(rowi + 2 * kKeys);  // [2] the slot's used keys: even ones, odd ones
 
   const int tid = threadIdx.x, warp = warp_id(), lane = lane_id();
   const int split = blockIdx.x;
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       tmem_ld_16x256b_x8(tmem + lane_off + s * kParts * kHeads, v);
       const float *f = factor + s * kKeys + k0;
       const float f0 = f[0], f1 = f[8];
+      const uint32_t mine = (k0 & 1 ? used[s].y : used[s].x) >> (k0 >> 1);  // bits 0 and 4: k0 and k0 + 8
       tmem_ld_wait();
       for (int x = 1; x < min(kParts, lay.nQ); ++x) {
         uint32_t u[32];
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
         w1 += __shfl_xor_sync(0xffffffffu, w1, o);
       }
       if ((lane & 3) == 0) {
-        if (f0 != INFINITY) add_weight(p, row, pos[0], w0);
-        if (f1 != INFINITY) add_weight(p, row, pos[1], w1);
+        if (mine & 1u) add_weight(p, row, pos[0], w0);
+        if (mine & 16u) add_weight(p, row, pos[1], w1);
       }
       pos[0] = next[0];
       pos[1] = next[1];
@@ -396,9 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       float v[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        v[x] = !live[x] ? INFINITY
+        v[x] = !live[x] ? 0.f
                         : (F == kLatBf16 ? 1.f : (F == kLatE4m3 ? __uint_as_float(f[x]) : pow2i(l4_exponent(f[x]))));
       *reinterpret_cast<float2 *>(&factor[(j & 1) * kKeys + 2 * lane]) = make_float2(v[0], v[1]);
+      const uint32_t even = __ballot_sync(0xffffffffu, live[0]), odd = __ballot_sync(0xffffffffu, live[1]);
+      if (lane == 0) used[j & 1] = make_uint2(even, odd);
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[j & 1]);
       return true;
