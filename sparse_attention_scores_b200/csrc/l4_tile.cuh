@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include "latent4.cuh"
+#include "warp_wait.cuh"
 
 namespace dsa {
 
@@ -51,25 +52,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0u;
-}
-// bounded wait that also gives up as soon as another role has failed
-__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
-                                             volatile uint32_t *failed) {
-  // the first tries do without the timer, whose reading takes hundreds of cycles
-#pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*failed) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
-      *failed = 1u;
-      return false;
-    }
-  }
 }
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {

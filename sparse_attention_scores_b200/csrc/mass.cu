@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
       pos[0] = next[0];
       pos[1] = next[1];
     }
-    if (nh > 0 && !*failed) publish(nh - 1);
+    if (nh > 0 && !warp_failed(failed)) publish(nh - 1);
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMA issue
     // S = L . Q^T, M = 64 keys, N = 64 heads, K = W; the converged warp computes
@@ -443,12 +443,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tile_u = __shfl_sync(0xffffffffu, tile, 0);
     const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
     const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;
-    bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
+    bool ok = nh == 0 || wait_or_fail(qready, 0u, p.wait_ns, failed);
     for (int j = 0; j < nh && ok; ++j) {
       const int s = j & 1;
-      if (!__all_sync(0xffffffffu, wait_or_fail(&full[s], (j >> 1) & 1, p.wait_ns, failed))) break;
-      if (j >= 2 && !__all_sync(0xffffffffu, wait_or_fail(&sread[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)))
-        break;
+      if (!wait_or_fail(&full[s], (j >> 1) & 1, p.wait_ns, failed)) break;
+      if (j >= 2 && !wait_or_fail(&sread[s], ((j >> 1) - 1) & 1, p.wait_ns, failed)) break;
       fence_proxy_async_smem();
       tc_fence_after();
       const uint32_t d = tm + s * kParts * kHeads;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const MassParams p) {
                       full_atoms >= kParts || k != 0 ? 1u : 0u);
       commit_elect(&sfull[s]);
     }
-    if (*failed) {
+    if (warp_failed(failed)) {
       commit_elect(bar_drain);
       mbar_wait(bar_drain, 0u, kDrainLimitNs);
     }

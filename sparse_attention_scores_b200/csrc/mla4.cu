@@ -409,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       }
       const bool need = from_z || (j > 0 && ((a0 != 1.f && h0 < p.H) || (a1 != 1.f && h1 < p.H)));
       if (bar_or(1, 32 * kSoftWarps, need || !alive)) {
-        from_z = from_z && alive;
-        if (bar_or(1, 32 * kSoftWarps, !alive)) break;
+        if (bar_or(1, 32 * kSoftWarps, !alive)) {
+          from_z = false;  // in every warp: none goes on below
+          break;
+        }
         if (j > 0) rescale(j, a0, a1);
         if (from_z) {
           l0 *= a0;
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
       pos[0] = next[0];
       pos[1] = next[1];
     }
-    if (nh > 0 && !*failed) publish(nh - 1);
+    if (nh > 0 && !warp_failed(failed)) publish(nh - 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA issue
     // The whole warp runs this and branches on votes, so that the descriptors
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     const uint32_t p_u = tile_u + lay.off_p;
     const int full_atoms = W / 64, tail = W / 16 - 4 * full_atoms;  // of the query; K steps after them
     const uint64_t d_q = smem_desc(tile_u + lay.off_q, 16, 1024, kLayoutSW128);
-    bool ok = nh == 0 || __all_sync(0xffffffffu, wait_or_fail(qready, 0u, p.wait_ns, failed));
+    bool ok = nh == 0 || wait_or_fail(qready, 0u, p.wait_ns, failed);
     int ns = 0, npv = 0;
     uint64_t t0 = 0;
     uint32_t spins = 0;
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
         }
       }
     }
-    if (*failed) {
+    if (warp_failed(failed)) {
       commit_elect(bar_drain);  // fires once every MMA issued above has completed
       mbar_wait(bar_drain, 0u, kDrainLimitNs);
     }
