@@ -36,6 +36,7 @@
 #include <math.h>
 
 #include "dsa_internal.h"
+#include "warp_wait.cuh"
 
 namespace dsa {
 namespace {
@@ -861,7 +862,8 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool v) {
       : "memory");
   return r != 0u;
 }
-// bounded wait that also gives up as soon as another role has failed
+// one thread's bounded wait (the MMA issuer's) that also gives up as soon as another
+// role has failed; whole warps take wait_or_fail, which votes
 __device__ __forceinline__ bool pipe_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
                                           volatile uint32_t *failed) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -998,8 +1000,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) mla_pipe_kernel(const MlaPara
       const int s = j & 1;
       const uint32_t par = (j >> 1) & 1;
       const bool active = (q4 >> 1) == s;
-      bool ok = pipe_wait(&sfull[s], par, p.wait_ns, failed) &&
-                pipe_wait(&full[s], par, p.wait_ns, failed);
+      bool ok = wait_or_fail(&sfull[s], par, p.wait_ns, failed) &&
+                wait_or_fail(&full[s], par, p.wait_ns, failed);
       tc_fence_after();
       float z[32];
       if (ok && active) {
@@ -1029,7 +1031,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) mla_pipe_kernel(const MlaPara
       // PV(j - 1) must be complete: the lo buffer is reused and, on a
       // rescale, the O accumulator must hold every earlier half
       bool ok2 = true;
-      if (j > 0) ok2 = pipe_wait(&empty[(j - 1) & 1], ((j - 1) >> 1) & 1, p.wait_ns, failed);
+      if (j > 0) ok2 = wait_or_fail(&empty[(j - 1) & 1], ((j - 1) >> 1) & 1, p.wait_ns, failed);
       if (ok2) {
         tc_fence_after();
         if (rescale) {
@@ -1080,8 +1082,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) mla_pipe_kernel(const MlaPara
       if (lane == 0) mbar_arrive(pready);
     }
     // the last PV must be complete before O is read
-    if (!*failed && nh > 0)
-      pipe_wait(&empty[(nh - 1) & 1], ((nh - 1) >> 1) & 1, p.wait_ns, failed);
+    if (nh > 0 && !warp_failed(failed))
+      wait_or_fail(&empty[(nh - 1) & 1], ((nh - 1) >> 1) & 1, p.wait_ns, failed);
   } else if (warp < kPipeMmaWarp) {
     // ------------------------------------------------------------ gather
     const int g = (warp - kPipeProdWarp0) >> 1;  // half-slot this group fills
@@ -1109,7 +1111,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) mla_pipe_kernel(const MlaPara
     int phys = resolve(g);
     for (int j = g; j < nh; j += 2) {
       const int u = j >> 1;
-      if (u >= 1 && !pipe_wait(&empty[g], (u - 1) & 1, p.wait_ns, failed)) break;
+      if (u >= 1 && !wait_or_fail(&empty[g], (u - 1) & 1, p.wait_ns, failed)) break;
       const uint32_t mask = __ballot_sync(0xffffffffu, phys >= 0);
       if (lane == 0) vmask[g * 2 + wl] = mask;
       if constexpr (kLat8) {

@@ -127,3 +127,13 @@ def test_whole_warps_wait_by_vote(name):
     assert not re.search(r"mbar_try_wait", text)
     assert not re.search(r"if \(\*failed\)", text)
     assert not re.search(r"&& !\*failed\) publish", text)
+
+
+def test_the_pipelined_bf16_and_e4m3_kernel_waits_by_vote_too():
+    """Its MMA issuer is one thread with a wait of its own; the other roles are whole warps."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "mla.cu")).read())
+    body = text[text.index("void __launch_bounds__(kPipeThreads, 1)"):]
+    issue = body.index("else if (lane == 0) {")
+    assert not re.search(r"pipe_wait|mbar_try_wait|mbar_wait\((?!bar_stall)", body[:issue])
+    assert not re.search(r"if \(!?\*failed", body[:issue])
+    assert len(re.findall(r"wait_or_fail\(", body[:issue])) == 5
