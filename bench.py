@@ -442,11 +442,11 @@ TRAFFIC = {
     ("topk", "glm5_decode_4x128k"): (2122240, "86581b1144701485"),
     ("topk", "glm5_prefill_2300"): (2234624, "86581b1144701485"),
     # mla_kernel + combine_kernel (the merge reads the split partials)
-    ("mla", "glm5_decode_8k"): (2508800 + 4231936, "5514fc61eba92590"),
-    ("mla", "glm5_decode_4x128k"): (9864704 + 16864256, "5514fc61eba92590"),
+    ("mla", "glm5_decode_8k"): (2508800 + 4231936, "18620338e0ce7eb4"),
+    ("mla", "glm5_decode_4x128k"): (9864704 + 16864256, "18620338e0ce7eb4"),
     # mla_pipe_kernel (rows merged inside clusters; prefill rows unsplit)
-    ("mla", "glm5_decode_b32_ragged"): (78396672, "5514fc61eba92590"),
-    ("mla", "glm5_prefill_2300"): (425517312, "5514fc61eba92590"),
+    ("mla", "glm5_decode_b32_ragged"): (78312448, "18620338e0ce7eb4"),
+    ("mla", "glm5_prefill_2300"): (425402624, "18620338e0ce7eb4"),
 }
 
 
