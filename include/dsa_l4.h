@@ -133,10 +133,11 @@ DSA_API dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float
  *             causal chunk >= q_pos0 + n_q (which is sequence 0: only row 0
  *             is written)
  * A position that a row holds twice counts twice.  Causal chunks add their
- * rows in 64-bit fixed point (steps of 2^-40), so the result does not depend
- * on the order in which the rows ran (a NaN weight, and one of 128 or more, which
- * no lse of the step's leaves, is added in fp32 instead); a decode row adds in
- * fp32, once per place.  Workspace: DSA_L4_OP_ATTENTION_MASS.  The three forms differ in
+ * rows in 64-bit fixed point, so the result does not depend on the order in
+ * which the rows ran (a NaN weight, and one of 128 or more, which no lse of the
+ * step's leaves, is added in fp32 instead).  A step is n_q 2^-56, n_q rounded up
+ * to a power of two (2^-47 for 512 rows); a weight below half of it adds nothing.
+ * A decode row adds in fp32, once per place.  Workspace: DSA_L4_OP_ATTENTION_MASS.  The three forms differ in
  * the latent cache they read: bf16, E4M3 with one scale per token, 4-bit. */
 DSA_API dsa_status_t dsa_attention_mass(const uint16_t *q, const uint16_t *latent_pages,
                                 const dsa_cache_t *cache, const int32_t *idx, const float *lse,

@@ -21,9 +21,15 @@ namespace dsa {
 namespace {
 
 constexpr int kSweep = 256;  // threads of the sweeps over positions
-// 2^40: 65,535 rows, the most a chunk has, of weights below kMostWeight stay below 2^63
-constexpr double kFixedOne = 1099511627776.0;
+// A chunk's sums are whole numbers of steps of 2^-f: the finest for which n_q rows
+// of weights below kMostWeight stay below 2^63 (f = 40 at 65,535 rows, the most a
+// chunk has, 47 at 512, 56 at one; a weight below half a step adds nothing)
 constexpr float kMostWeight = 128.f;
+inline int fixed_bits(int n_q) {
+  int c = 0;  // n_q <= 2^c
+  while ((static_cast<int64_t>(1) << c) < n_q) ++c;
+  return 63 - 7 - c;
+}
 
 struct MassParams {
   const uint16_t *q;
@@ -40,6 +46,7 @@ struct MassParams {
   int n_q, num_seqs, H, W, topk, nsplit;
   uint32_t cpr_inv, units_inv;  // inverses of 16-byte pieces per query head and per stored row, at 2^20
   float scale_log2, decay;
+  double fixed_one;  // 2^fixed_bits
   uint64_t wait_ns;
   int debug_stall;
   DevStatus *status;
@@ -70,7 +77,7 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
   if (pos < 0 || pos >= p.max_len) return;
   if (p.rows.causal && w < kMostWeight)
     atomicAdd(&p.fixed[pos], static_cast<unsigned long long>(
-                                 __double2ll_rn(static_cast<double>(w) * kFixedOne)));
+                                 __double2ll_rn(static_cast<double>(w) * p.fixed_one)));
   else
     atomicAdd(&p.mass_out[p.rows.causal ? pos : row * p.mass_ld + pos], w);
 }
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kSweep) fold_kernel(const MassParams p) {
   const int n = mass_len(p, 0);
   for (int s = blockIdx.x * kSweep + threadIdx.x; s < n; s += gridDim.x * kSweep)
     p.mass_out[s] = static_cast<float>(static_cast<double>(p.mass_out[s]) +
-                                       static_cast<double>(p.fixed[s]) * (1.0 / kFixedOne));
+                                       static_cast<double>(p.fixed[s]) * (1.0 / p.fixed_one));
 }
 
 template <int F>
@@ -534,6 +541,7 @@ dsa_status_t launch_mass(const MassLaunch &a, cudaStream_t stream) {
   p.cpr_inv = query_pieces_inverse(p.W);
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.decay = a.decay;
+  p.fixed_one = ldexp(1.0, fixed_bits(a.n_q));
   p.wait_ns = wait_limit_ns();
   p.debug_stall = debug_stall() == static_cast<int>(kKernMass) ? 1 : 0;
   p.status = a.status;

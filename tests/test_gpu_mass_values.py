@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import sparse_attention_scores_b200 as dsa
-from tests.l4_testutil import Paged, bf16_cuda, select, to_bf16
+from tests.l4_testutil import Paged, U, bf16_cuda, logit_bound, random_l4, select, to_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,52 @@ def test_a_token_of_infinite_scale_shows_in_the_mass(causal):
     rest = np.arange(ld) != tok
     assert np.array_equal(now[:, rest], plain[:, rest])
     assert dsa.workspace_check(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("n,log2_w", [(1, -53), (4, -48), (512, -44), (700, -43)])
+def test_small_weights_of_a_chunk_are_not_lost(n, log2_w):
+    """lse far above the logits: weights of about 2^log2_w, which a chunk of n rows
+    adds in steps of 2^-56 times n (rounded up to a power of two)."""
+    rng = np.random.default_rng(n)
+    H, R, P, k, pos0 = 2, 64, 16, 8, 20
+    pg = Paged([pos0 + n], seed=2)
+    pool, values = random_l4(rng, pg.num_pages, R + P)
+    q = to_bf16(rng.standard_normal((n, H, R + P)))
+    idx = select(rng, [pos0 + t + 1 for t in range(n)], k)
+    lse = np.zeros((n, H), np.float32)
+    ref, tol = np.zeros(pos0 + n), np.zeros(pos0 + n)
+    for t in range(n):
+        L = values[pg.rows(0, idx[t])]
+        z = 0.125 * (q[t] @ L.T)
+        lse[t] = z.max(1) - log2_w * np.log(2)
+        w = np.exp(z - lse[t].astype(np.float64)[:, None])
+        # a head's weight: its logit's error, the exponential's 2^-19, the rounding of
+        # an argument below 128; then half a step for the row
+        rel = logit_bound(q[t], L, 0.125) + 2.0 ** -19 + 144 * U
+        np.add.at(ref, idx[t], w.sum(0))
+        np.add.at(tol, idx[t], (w * rel).sum(0) + 2.0 ** (np.ceil(np.log2(n)) - 57))
+    cache, dims = pg.cache(), dsa.Dims(n, 1, 32, k, H, R, P, 1, pos0, 0.125)
+    got = torch.zeros(1, pos0 + n, device="cuda")
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    dsa.dsa_attention_mass_l4(bf16_cuda(q), torch.from_numpy(pool).cuda(), cache, torch.from_numpy(idx).cuda(),
+                              torch.from_numpy(lse).cuda(), dims, 1.0, None, got, ws)
+    assert dsa.workspace_check(ws) == (0, 0)
+    g = got[0].double().cpu().numpy()
+    assert (np.abs(g - ref) <= tol + 4 * U * ref).all(), (np.abs(g - ref) - tol).max()
+    assert ref.max() > 8 * tol[ref.argmax()]  # a sum that lost its weights would show
+
+
+def test_the_largest_chunk_does_not_overflow():
+    """65,535 rows that give one token the most weight lse of the step's can leave."""
+    n, H, R, P = 65535, 64, 64, 0
+    pg = Paged([n], seed=1)
+    pool = torch.zeros(pg.num_pages, 64, 48, dtype=torch.uint8, device="cuda")
+    q = torch.zeros(n, H, R, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(n, 1, dtype=torch.int32, device="cuda")  # every row keeps the first token only
+    lse = torch.zeros(n, H, device="cuda")
+    cache, dims = pg.cache(), dsa.Dims(n, 1, 32, 1, H, R, P, 1, 0, 0.125)
+    got = torch.zeros(1, n, device="cuda")
+    ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, dims, cache)
+    dsa.dsa_attention_mass_l4(q, pool, cache, idx, lse, dims, 1.0, None, got, ws)
+    assert dsa.workspace_check(ws) == (0, 0)
+    assert float(got[0, 0]) == float(np.float32(n * H)) and float(got[0, 1:].abs().max()) == 0
