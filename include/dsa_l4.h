@@ -125,7 +125,11 @@ DSA_API dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float
  *             position outside the row's context is skipped and flagged)
  *   lse       [n_q, H] fp32, the step's; a row with lse = -inf adds nothing
  *   decay     finite, >= 0
- *   mass_in   [num_seqs, mass_ld] fp32, or NULL for zeros
+ *   mass_in   [num_seqs, mass_ld] fp32, or NULL for zeros.  Every entry s < len(b)
+ *             is read: a token that was appended since the sums were last written
+ *             has to hold 0 there.  Neither an append nor an eviction clears it,
+ *             so a buffer that held a longer sequence before an eviction still
+ *             holds the sums of tokens that are gone
  *   mass_out  [num_seqs, mass_ld] fp32; may be mass_in, else apart from it.  Entries s < len(b) are
  *             written (len(b): seq_lens[b], at most max_seq_len; for a causal
  *             chunk q_pos0 + n_q); entries past that are left untouched, and
@@ -199,7 +203,8 @@ typedef struct {
  *   new_lens  [num_seqs] int32 output; may be cache->seq_lens
  *   kept      [num_seqs, budget] int32 output: the kept positions, ascending,
  *             -1 padded; may be NULL
- * Destination rows, masses and pages past new_lens[b] are left untouched.  A
+ * Destination rows, masses and pages past new_lens[b] are left untouched: set
+ * mass_dst[b, s] to 0 before dsa_attention_mass reads it for a new token s.  A
  * source or destination page id out of range skips that row and is reported
  * as DSA_ERR_DEVICE_CHECK.  Workspace: DSA_L4_OP_CACHE_EVICT. */
 DSA_API dsa_status_t dsa_cache_evict(const dsa_pool_t *pools, int32_t n_pools,

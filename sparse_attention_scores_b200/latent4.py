@@ -267,7 +267,8 @@ def dsa_attention_mass(q, latent_pages, cache, idx, lse, dims, decay, mass_in, m
                        stream=None) -> None:
     """Add the attention weight each kept token received to a running sum per
     token: mass_out = decay * mass_in + sum over heads of exp(z - lse), mass_*
-    [sequences, positions] fp32 (mass_in None: zeros; mass_out may be mass_in)."""
+    [sequences, positions] fp32 (mass_in None: zeros; mass_out may be mass_in).
+    A token appended since has to hold 0 in mass_in: nothing else clears it."""
     _ready or l4_lib()
     dev = _device()
     lat = (_arg(latent_pages, "latent_pages", _bf16, dev,
@@ -311,8 +312,9 @@ def dsa_cache_evict(pools, cache, evict: Eviction, mass, dst_block_table, mass_d
     pools: up to four (source, destination) pairs of page pools [pages, 64, ...]
     (any type; a per-token scale is a pool [pages, 64]); mass [sequences,
     positions] fp32; dst_block_table [sequences, pages] int32; mass_dst
-    [sequences, positions] fp32 or None; new_lens [sequences] int32; kept
-    [sequences, budget] int32 or None.
+    [sequences, positions] fp32 or None, left as it was past new_lens (zero an
+    entry before the mass of a new token is added to it); new_lens [sequences]
+    int32; kept [sequences, budget] int32 or None.
     """
     L, dev = _ready or l4_lib(), _device()
     c, _, w, n = _common(cache, None, ws, dev)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import sparse_attention_scores_b200 as dsa
+from oracle import l4_oracle as l4
 from tests.l4_testutil import Paged, U, bf16_cuda, logit_bound, random_l4, select, to_bf16
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,55 @@ def test_the_largest_chunk_does_not_overflow():
     dsa.dsa_attention_mass_l4(q, pool, cache, idx, lse, dims, 1.0, None, got, ws)
     assert dsa.workspace_check(ws) == (0, 0)
     assert float(got[0, 0]) == float(np.float32(n * H)) and float(got[0, 1:].abs().max()) == 0
+
+
+def test_sums_over_evictions_in_two_swapped_buffers():
+    """Decode steps and evictions in turn, the masses moving between two buffers that
+    hold other sums before: with a new token's entry set to 0 the sums are those of
+    the tokens that are there."""
+    rng = np.random.default_rng(4)
+    H, R, P, k, budget, pages = 16, 64, 16, 40, 96, 12
+    W, scale = R + P, 0.125
+    pool = torch.zeros(pages, 64, l4.row_bytes(W), dtype=torch.uint8, device="cuda")
+    keys = torch.zeros(pages, 64, 32, dtype=torch.bfloat16, device="cuda")
+    tables = torch.tensor([[3, 1, 8], [5, 2, 9]], dtype=torch.int32, device="cuda")
+    sums = [torch.full((1, 192), 1000.0 + i, device="cuda") for i in range(2)]
+    seq = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new_lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(1, budget, dtype=torch.int32, device="cuda")
+    one = dsa.Dims(1, 1, 32, k, H, R, P, 0, 0, scale)
+    values, ref, tol = np.zeros((0, W)), np.zeros(0), np.zeros(0)
+    at = 0
+    for length in (130, 110, 140):  # up to so many tokens, then an eviction
+        cache = dsa.PagedCache(seq, tables[at:at + 1], pages, 192)
+        ws = dsa.l4_workspace(dsa.L4_OP_ATTENTION_MASS, one, cache)
+        while len(values) < length:
+            seq += 1
+            row = to_bf16(rng.standard_normal((1, W)))
+            dsa.dsa_cache_append_l4(torch.zeros(1, 32, dtype=torch.bfloat16, device="cuda"), bf16_cuda(row), keys, pool,
+                                    cache, one, ws)
+            sums[at][0, len(values)] = 0
+            values = np.concatenate([values, l4.quantise(row)[1]])
+            ref, tol = np.append(ref, 0.0), np.append(tol, 0.0)
+            q = to_bf16(rng.standard_normal((1, H, W)))
+            idx = select(rng, [len(values)], k)
+            pos = idx[0][idx[0] >= 0]
+            L = values[pos]
+            lse = l4.attention(q[0], L, R, scale)[1].astype(np.float32)
+            dsa.dsa_attention_mass_l4(bf16_cuda(q), pool, cache, torch.from_numpy(idx).cuda(),
+                                      torch.from_numpy(lse[None]).cuda(), one, 0.875, sums[at], sums[at], ws)
+            ref, tol = 0.875 * ref, 0.875 * tol + U * ref
+            l4.add_mass(ref, pos, q[0], L, lse, scale)
+            w = np.exp(scale * (q[0] @ L.T) - lse.astype(np.float64)[:, None])
+            np.add.at(tol, pos, (w * (logit_bound(q[0], L, scale) + 2.0 ** -19 + 144 * U)).sum(0))
+            tol = tol + 2 * U * ref
+        assert dsa.workspace_check(ws) == (0, 0)
+        assert (np.abs(sums[at][0, :length].double().cpu().numpy() - ref) <= tol).all()
+        ws = dsa.l4_workspace(dsa.L4_OP_CACHE_EVICT, None, cache)
+        dsa.dsa_cache_evict([(pool, pool), (keys, keys)], cache, dsa.Eviction(budget, 2, 10), sums[at],
+                            tables[1 - at:2 - at], sums[1 - at], new_lens, kept, ws)
+        assert dsa.workspace_check(ws) == (0, 0)
+        left = kept[0].cpu().numpy()
+        assert np.array_equal(left, l4.evict_keep(sums[at][0, :length].cpu().numpy(), budget, 2, 10))
+        values, ref, tol = values[left], ref[left], tol[left]
+        at, seq = 1 - at, new_lens.clone()
