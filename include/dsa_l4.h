@@ -93,9 +93,12 @@ DSA_API dsa_status_t dsa_cache_read_l4(const uint8_t *latent4_pages, const dsa_c
  * cores exactly; q enters as fp16 after a power-of-two scale per query row, so
  * a q element is carried exactly unless it is below 2^-28 of the row's largest
  * magnitude (then to 2^-39 of it); the softmax weights enter as two fp16 terms
- * (22 bits); sums are fp32, which the tensor cores truncate rather than round:
- * against float64, out is off by about 1e-6 of its largest magnitude at 32 rows
- * of 2,048 kept tokens, 2e-6 over a 2,300-token prefill.  q must be finite.
+ * (22 bits), and what a token adds to out is lost below 2^-31 of the row's
+ * largest such product; sums are fp32, which the tensor cores truncate rather
+ * than round: against float64, out is off by up to 2e-6 of its largest magnitude
+ * at 32 rows of 2,048 kept tokens, 4e-6 where one CTA takes 1,024 or more (columns
+ * from 256 on, whose two terms share a sum, about twice what the others are), and
+ * lse by 2e-6.  q must be finite.
  * Workspace: DSA_L4_OP_SPARSE_MLA. */
 DSA_API dsa_status_t dsa_sparse_mla_decode_l4(const uint16_t *q, const uint8_t *latent4_pages,
                                       const dsa_cache_t *cache, const int32_t *idx,
@@ -141,7 +144,8 @@ DSA_API dsa_status_t dsa_attention_forward_l4(const uint16_t *q_idx, const float
  * which the rows ran (a NaN weight, and one of 128 or more, which no lse of the
  * step's leaves, is added in fp32 instead).  A step is n_q 2^-56, n_q rounded up
  * to a power of two (2^-47 for 512 rows); a weight below half of it adds nothing.
- * A decode row adds in fp32, once per place.  Workspace: DSA_L4_OP_ATTENTION_MASS.  The three forms differ in
+ * A decode row adds in fp32, once per place.  Against float64, with the lse given, a mass is off
+ * by about 1e-6 of the largest (its logits are tensor-core sums as above).  Workspace: DSA_L4_OP_ATTENTION_MASS.  The three forms differ in
  * the latent cache they read: bf16, E4M3 with one scale per token, 4-bit. */
 DSA_API dsa_status_t dsa_attention_mass(const uint16_t *q, const uint16_t *latent_pages,
                                 const dsa_cache_t *cache, const int32_t *idx, const float *lse,
