@@ -10,7 +10,6 @@ namespace dsa {
 
 constexpr int kL4Block = 16;      // columns per block scale
 constexpr int kL4MaxExp = 60;     // |e| of a row's power of two
-constexpr float kL4RowMax = 2688.f;  // 6 * 448: the largest |value| of a row with e = 0
 
 // position -> pool row of query row r (its sequence: r, or 0 in a causal
 // chunk); -1 for an unused slot, and for a position outside [0, limit) or a
@@ -73,7 +72,8 @@ __device__ __forceinline__ int l4_exponent(uint32_t byte) {
 // 2^e for |e| <= 126
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// least e with amax <= 2688 * 2^e = 1.3125 * 2^(e + 11), clamped; 0 for amax = 0
+// least e with amax <= 2688 * 2^e, clamped; 0 for amax = 0.  2688 = 6 * 448, the
+// largest |s v|, is 1.3125 * 2^11: mantissa bits 0x280000
 __device__ __forceinline__ int l4_row_exponent(float amax) {
   if (amax == 0.f) return 0;
   const uint32_t u = __float_as_uint(amax);

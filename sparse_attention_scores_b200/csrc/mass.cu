@@ -43,7 +43,7 @@ struct MassParams {
   unsigned long long *fixed;
   int64_t mass_ld;
   int max_len;
-  int n_q, num_seqs, H, W, topk, nsplit;
+  int n_q, H, W, topk, nsplit;
   uint32_t cpr_inv, units_inv;  // inverses of 16-byte pieces per query head and per stored row, at 2^20
   float scale_log2, decay;
   double fixed_one;  // 2^fixed_bits
@@ -88,7 +88,8 @@ __device__ __forceinline__ void add_weight(const MassParams &p, int row, int pos
 // tensor cores truncate each accumulation towards zero, and the errors of a
 // chain add up in the logit: 512 causal rows of 2,048 keys are off by 1.4e-6
 // with one chain of 36, 6.5e-7 with two of 18 (3% slower), 3.4e-7 with four (6%);
-// fp32 additions give 6e-8.
+// fp32 additions give 6e-8.  Two were chosen: what is left is below what the
+// attention's own sums lose.
 constexpr int kMisc = 2048;
 constexpr int kParts = 2;
 struct Layout {
@@ -534,7 +535,6 @@ dsa_status_t launch_mass(const MassLaunch &a, cudaStream_t stream) {
   p.mass_ld = a.mass_ld;
   p.max_len = a.max_len;
   p.n_q = a.n_q;
-  p.num_seqs = a.num_seqs;
   p.H = a.H;
   p.W = a.R + a.P;
   p.topk = a.topk;

@@ -108,7 +108,11 @@ __host__ __device__ inline Layout layout_of(int R, int W) {
   return l;
 }
 // Tensor memory: S of slot s at columns 64 s, then the CTA's n blocks of O^T,
-// `wide` of which keep the sums of the two terms side by side.
+// `wide` of which keep the sums of the two terms side by side.  In the others
+// each small lo product truncates the large sum once more: 1,024 keys a CTA leave
+// up to 2.1e-6 of the largest element in columns 0-255 and 4.1e-6 in 256-511, 512
+// keys 1.5e-6 and 2.3e-6.  Four wide blocks would need 640 of 512 columns; one
+// buffer of S would make room for them, and end the overlap of S and softmax.
 constexpr int kWideCols = 128;  // columns of a wide block, against 64
 struct Blocks {
   int n, wide;
