@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla4_kernel(const Mla4Params p) {
     // The same from the first slot with a far key on, l apart from the weights (a
     // second exponential per key).  A rolled loop of its own, from S in tensor
     // memory: inside the loop above, or unrolled beside it, it took registers from
-    // every row (2,300 causal rows 883 and 845 us, 823 so, 813 without it).
+    // every row (2,300 causal rows 883 and 845 us, 823 so, 813 without it; 819 since
+    // the waits vote).  With far keys in every row: 997.
     if (j < nh && from_z) {
       float n0 = m0, n1 = m1;  // what l is relative to
       for (; j < nh; ++j) {
